@@ -243,6 +243,9 @@ def prepare(case, seed):
         s["weights_out"] = torch.zeros_like(s["weights"])
         s["positions_out"] = torch.full_like(s["positions"], -1)
         s["kept"] = torch.empty((B, Hkv, case["n_keep"]), dtype=torch.int32, device="cuda")
+        if own:
+            import tiled_attention_24_b200 as ta
+            s["ws"] = torch.empty(ta.attn_kv4_evict_workspace_bytes(B, Hkv, cap, case["n_keep"]), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -333,7 +336,7 @@ def _evict(s):
     if own:
         import tiled_attention_24_b200 as ta
         ta.attn_kv4_evict(s["kc"], s["ks"], s["vc"], s["vs"], s["weights"], s["positions"], s["seqlens"], s["next_pos"],
-                          s["weights_out"], s["positions_out"], s["kept"], c["n_recent"])
+                          s["weights_out"], s["positions_out"], s["kept"], c["n_recent"], s["ws"])
     else:
         B, Hkv, cap = s["weights"].shape
         n_keep = c["n_keep"]
