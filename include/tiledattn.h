@@ -389,6 +389,112 @@ ATTN_API int attn_fwd_fp8(const uint8_t* q, const float* q_scale, const uint8_t*
                           int Nkv, int d, int causal, float scale, int rotated, void* stream);
 
 /*
+ * The 4-bit key/value cache.  One cache holds, for every (batch, cache head),
+ * `capacity` rows (slots) of d channels as signed 4-bit codes with one bf16
+ * scale per group of 32 consecutive channels (4.5 bits a value):
+ *   s = bf16(amax / 7) (IEEE fp32 divide, round to nearest even twice),
+ *   c = clamp(rne(x / s), -7, 7), value c * s; s == 0 gives c = 0; a group
+ *   that holds an infinity or a NaN gets s = NaN, c = 0.
+ *   kc, vc         uint8 [B][Hkv][capacity][d / 2] codes: byte u*(d/16) + 2g + h
+ *                  of a row (u < 8, g < d/32, h < 2) holds channel
+ *                  32g + 4u + 2h in its low nibble, the next in its high one;
+ *   ks, vs         bf16 [B][Hkv][capacity][d / 32] scales;
+ *   seqlens        int32 [B]: slots [0, seqlens[b]) are live (clamped to
+ *                  [0, capacity] on the device), all others are never used;
+ *   weights        fp32 [B][Hkv][capacity], the accumulated attention weight of
+ *                  a slot, and positions int32 [B][Hkv][capacity], the token
+ *                  position it holds: needed where a cache is to be evicted.
+ * d in {64, 128}; capacity a positive multiple of 16; code arrays 16-byte, scale
+ * arrays 16-byte aligned.  The order of the slots does not matter to attention;
+ * after an eviction they are not in the order of the tokens.
+ * B * Hkv * capacity, B * Hkv * n and B * Hkv * n_keep are at most 2^31 - 1.
+ *
+ * attn_kv4_append -- quantise n new tokens of every sequence and write them:
+ * token i < counts[b] goes to slot starts[b] + i (tokens whose slot is not in
+ * [0, capacity) are dropped).  With weights / positions the slot gets weight 0
+ * and position next_pos[b] + i.  The caller then advances its seqlens.
+ *   k, v bf16 [B][Hkv][n][d] (16-byte aligned); starts, counts, next_pos int32
+ *   [B] DEVICE arrays; counts NULL: n tokens each; weights, positions may be
+ *   NULL; next_pos is needed with positions.
+ */
+ATTN_API int attn_kv4_append(const attn_bf16_t* k, const attn_bf16_t* v, uint8_t* kc, attn_bf16_t* ks, uint8_t* vc,
+                             attn_bf16_t* vs, const int* starts, const int* counts, float* weights, int* positions,
+                             const int* next_pos, int B, int Hkv, int n, int capacity, int d, void* stream);
+
+/*
+ * attn_kv4_read -- the values of n slots of one code array as bf16 (for
+ * attn_fwd_gqa over a prefix that is already in the cache):
+ * out[b][h][i] = bf16(code * scale) of slot starts[b] + i; zeros where that is
+ * not in [0, capacity).  starts int32 [B] DEVICE, NULL: from slot 0.
+ */
+ATTN_API int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn_bf16_t* out, const int* starts, int B,
+                           int Hkv, int n, int capacity, int d, void* stream);
+
+/*
+ * attn_decode_kv4 -- split-KV decode (as attn_decode_varlen) over a 4-bit
+ * cache: one query row per (batch, query head), Hq query heads sharing Hkv
+ * cache heads, live slots [0, seqlens[b]).  With weights, every live slot's
+ * weight grows by the sum of the softmax probabilities of its cache head's
+ * query heads.  A sequence without live slots gets O = 0, LSE = -inf.
+ *   q, o bf16 [B][Hq][1][d]; lse fp32 [B][Hq]; seqlens int32 [B] DEVICE;
+ *   weights fp32 [B][Hkv][capacity] or NULL; 1 <= num_splits <= 1024
+ *   (attn_decode_kv4_splits: a good choice for the sizes); workspace of
+ *   attn_decode_kv4_workspace_bytes(...) bytes, 16-byte aligned (with_weights:
+ *   whether weights is given).  Calls that share a workspace must not overlap
+ *   in time.
+ */
+ATTN_API int attn_decode_kv4_splits(int B, int Hq, int Hkv, int capacity, int d);
+ATTN_API size_t attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int capacity, int d, int num_splits,
+                                                int with_weights);
+ATTN_API int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* ks, const uint8_t* vc,
+                             const attn_bf16_t* vs, attn_bf16_t* o, float* lse, float* weights, const int* seqlens,
+                             int B, int Hq, int Hkv, int capacity, int d, float scale, int num_splits,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_key_weights -- the attention weight that each key of a prompt received:
+ * w[b][g][j] = sum over the query heads h of key/value head g and the query
+ * rows i of exp(scale q_hi . k_j - lse_hi), masked as attn_fwd_gqa; lse is that
+ * call's output for the same arguments.  Nq < Nkv with causal weighs the last
+ * Nq queries only (hand q and lse of that window).
+ *   q bf16 [B][Hq][Nq][d], k bf16 [B][Hkv][Nkv][d], lse fp32 [B][Hq][Nq];
+ *   weights: rows of Nkv floats, weights_stride >= Nkv floats apart, one per
+ *   (batch, key/value head) (a cache's weights: weights_stride = capacity);
+ *   accumulate != 0 adds to what is there, 0 overwrites it.
+ *   seqlens int32 [B] DEVICE or NULL: a padded batch; only tokens at positions
+ *   below seqlens[b] count (query i has position i + Nkv - Nq), keys beyond get
+ *   weight 0.  workspace: attn_key_weights_workspace_bytes(...) bytes (may be
+ *   0), 16-byte aligned.
+ */
+ATTN_API size_t attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d);
+ATTN_API int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* lse, float* weights,
+                              const int* seqlens, int B, int Hq, int Hkv, int Nq, int Nkv, int d, int causal,
+                              int accumulate, float scale, long long weights_stride, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * attn_kv4_evict -- shrink every (batch, cache head) with more than n_keep live
+ * slots to n_keep: kept are the slots whose position is at least
+ * next_pos[b] - n_recent, then those of the largest weight; equal weights go
+ * to the lower slot, -0 equals +0, a NaN weight ranks with -infinity.  In place
+ * and without a copy of the cache: kept slots below n_keep stay where they
+ * are, the r-th kept slot at or beyond n_keep moves into the r-th free slot
+ * below it.
+ *   kept int32 [B][Hkv][n_keep] out: the old slot of each new one (-1 where
+ *   fewer slots are live).  weights_out, positions_out [B][Hkv][capacity]:
+ *   entries of the first min(seqlens[b], n_keep) slots are written; they may be
+ *   the arrays weights, positions themselves.  Slots >= n_keep are left as
+ *   they were.  The caller then sets seqlens[b] to min(seqlens[b], n_keep).
+ *   1 <= n_keep <= capacity, 0 <= n_recent <= n_keep; workspace:
+ *   attn_kv4_evict_workspace_bytes(...) bytes, 16-byte aligned.
+ */
+ATTN_API size_t attn_kv4_evict_workspace_bytes(int B, int Hkv, int capacity, int n_keep);
+ATTN_API int attn_kv4_evict(uint8_t* kc, attn_bf16_t* ks, uint8_t* vc, attn_bf16_t* vs, const float* weights,
+                            const int* positions, const int* seqlens, const int* next_pos, float* weights_out,
+                            int* positions_out, int* kept, int B, int Hkv, int capacity, int d, int n_keep,
+                            int n_recent, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_check_status -- synchronise `stream`, read the device status word
  * written by the kernels' watchdog (ATTN_OK or ATTN_ERR_TIMEOUT; in the debug
  * build also ATTN_ERR_BOUNDS), clear it and return it; also returns

@@ -15,7 +15,10 @@ from ._binding import (AttnError, LIB_PATH, attn_check_status, attn_debug_counte
                        attn_fwd, attn_fwd_fp8, attn_fwd_gqa, attn_fwd_varlen, attn_decode_varlen, attn_quantize_fp8, attn_quantize_int4, attn_bwd, attn_bwd_fp8p, attn_bwd_workspace_bytes,
                        attn_fwd_fp4, attn_fwd_int8, attn_int8_scores, attn_nvfp4_codes_bytes,
                        attn_nvfp4_sf_bytes, attn_quantize_int8, attn_quantize_nvfp4, attn_set_wait_limit_ns,
-                       attn_status_string, attn_version, attn_watchdog_selftest, load)
+                       attn_status_string, attn_version, attn_watchdog_selftest, load,
+                       attn_kv4_append, attn_kv4_read, attn_decode_kv4, attn_decode_kv4_splits,
+                       attn_decode_kv4_workspace_bytes, attn_key_weights, attn_key_weights_workspace_bytes,
+                       attn_kv4_evict, attn_kv4_evict_workspace_bytes)
 
 __all__ = ["load", "attn_fwd", "attn_decode", "attn_decode_workspace_bytes", "attn_check_status",
            "attn_set_wait_limit_ns", "attn_watchdog_selftest", "attn_version", "attn_status_string",
@@ -26,6 +29,9 @@ __all__ = ["load", "attn_fwd", "attn_decode", "attn_decode_workspace_bytes", "at
            "attn_bwd", "attn_bwd_fp8p", "attn_bwd_workspace_bytes", "backward",
            "attn_quantize_fp8", "attn_fwd_fp8", "quantize_fp8", "forward_fp8", "hadamard_signs",
            "attn_fwd_varlen", "attn_decode_varlen", "forward_varlen", "decode_varlen",
+           "attn_kv4_append", "attn_kv4_read", "attn_decode_kv4", "attn_decode_kv4_splits",
+           "attn_decode_kv4_workspace_bytes", "attn_key_weights", "attn_key_weights_workspace_bytes",
+           "attn_kv4_evict", "attn_kv4_evict_workspace_bytes", "KV4Cache", "decode_kv4", "key_weights",
            "attn_debug_counters", "DIRECT_P", "QUANT_AFTER_EXP"]
 
 DIRECT_P, QUANT_AFTER_EXP = 0, 1
@@ -204,3 +210,120 @@ def forward_fp4(q, k, v, causal: bool = False, scale: float | None = None, p_mod
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     attn_fwd_fp4(qc, qs, kc, ks, vc, vs, o, lse, B, H, Nq, Nkv, causal, scale, p_mode, stream)
     return o, lse
+
+
+class KV4Cache:
+    """A 4-bit key/value cache: codes kc, vc (uint8 [B,Hkv,capacity,d/2]) with scales ks,
+    vs (bf16 [B,Hkv,capacity,d/32]), the live slots seqlens and next token positions
+    next_pos of each sequence (int32 [B]) and, with ``track``, the accumulated
+    attention weights and the positions per slot that an eviction goes by.
+
+    ``capacity`` is rounded up to a multiple of 16.  The host keeps an upper bound of
+    the lengths, so that an append that may not fit is refused without a
+    synchronisation (on the device, tokens beyond the capacity would be dropped)."""
+
+    def __init__(self, B: int, Hkv: int, capacity: int, d: int, device="cuda", track: bool = True):
+        if B < 1 or Hkv < 1 or capacity < 1 or d not in (64, 128):
+            raise ValueError(f"B, Hkv, capacity must be positive and d 64 or 128, got {B}, {Hkv}, {capacity}, {d}")
+        capacity = -(-capacity // 16) * 16
+        self.B, self.Hkv, self.capacity, self.d = B, Hkv, capacity, d
+        z = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+        self.kc, self.vc = (z((B, Hkv, capacity, d // 2), torch.uint8) for _ in range(2))
+        self.ks, self.vs = (z((B, Hkv, capacity, d // 32), torch.bfloat16) for _ in range(2))
+        self.seqlens, self.next_pos = z((B,), torch.int32), z((B,), torch.int32)
+        self.weights = z((B, Hkv, capacity), torch.float32) if track else None
+        self.positions = z((B, Hkv, capacity), torch.int32) if track else None
+        self.length_bound = 0
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None, stream=None):
+        """Append n tokens (k, v bf16 [B,Hkv,n,d]) to every sequence, or the first
+        ``counts[b]`` (int32 [B], 0 to n) of them."""
+        n = k.shape[2]
+        if self.length_bound + n > self.capacity:
+            raise ValueError(f"{n} more tokens may not fit: up to {self.length_bound} of {self.capacity} slots are in use")
+        attn_kv4_append(k, v, self.kc, self.ks, self.vc, self.vs, self.seqlens, counts, self.weights, self.positions,
+                        self.next_pos if self.positions is not None else None, stream)
+        with _stream_context(stream, k.device):
+            by = n if counts is None else counts.clamp(0, n)
+            self.seqlens.add_(by)
+            self.next_pos.add_(by)
+        self.length_bound += n
+
+    def read(self, n: int | None = None, stream=None):
+        """(k, v) of the first n slots (default: the length bound) as bf16 [B,Hkv,n,d]."""
+        n = self.length_bound if n is None else n
+        out = []
+        with _stream_context(stream, self.kc.device):
+            for c, s in ((self.kc, self.ks), (self.vc, self.vs)):
+                x = torch.empty((self.B, self.Hkv, n, self.d), dtype=torch.bfloat16, device=c.device)
+                attn_kv4_read(c, s, x, None, stream)
+                out.append(x)
+        return tuple(out)
+
+    def evict(self, n_keep: int, n_recent: int = 0, stream=None):
+        """Keep at most n_keep slots per (batch, cache head): the n_recent newest tokens,
+        then those of the largest accumulated weight.  Returns the old slot of each
+        kept one, int32 [B,Hkv,n_keep] (-1 where a sequence is shorter)."""
+        if self.weights is None:
+            raise ValueError("this cache does not track weights: nothing to evict by")
+        if not 1 <= n_keep <= self.capacity:
+            raise ValueError(f"n_keep must be from 1 to {self.capacity}, got {n_keep}")
+        with _stream_context(stream, self.kc.device):
+            kept = torch.empty((self.B, self.Hkv, n_keep), dtype=torch.int32, device=self.kc.device)
+            ws = torch.empty(attn_kv4_evict_workspace_bytes(self.B, self.Hkv, self.capacity, n_keep),
+                             dtype=torch.uint8, device=self.kc.device)
+            attn_kv4_evict(self.kc, self.ks, self.vc, self.vs, self.weights, self.positions, self.seqlens,
+                           self.next_pos, self.weights, self.positions, kept, n_recent, ws, stream)
+            self.seqlens.clamp_(max=n_keep)
+        self.length_bound = min(self.length_bound, n_keep)
+        return kept
+
+
+def _stream_context(stream, device):
+    """torch's own small operations (allocation, lengths) on the stream of the kernels."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def decode_kv4(q: torch.Tensor, cache: KV4Cache, scale: float | None = None, num_splits: int | None = None,
+               workspace: torch.Tensor | None = None, track: bool | None = None, stream=None):
+    """Allocate O, LSE (and a workspace if none is given) and run ``attn_decode_kv4`` over
+    the cache; its weights grow by this step's unless ``track`` is False."""
+    B, Hq, _, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    weights = cache.weights if track is None or track else None
+    if track and weights is None:
+        raise ValueError("this cache does not track weights")
+    if num_splits is None:
+        num_splits = attn_decode_kv4_splits(B, Hq, cache.Hkv, cache.capacity, d)
+    with _stream_context(stream, q.device):
+        if workspace is None:
+            nbytes = attn_decode_kv4_workspace_bytes(B, Hq, cache.Hkv, cache.capacity, d, num_splits, weights is not None)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
+        attn_decode_kv4(q, cache.kc, cache.ks, cache.vc, cache.vs, o, lse, cache.seqlens, scale, num_splits,
+                        workspace, weights, stream)
+    return o, lse
+
+
+def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, causal: bool = False, scale: float | None = None,
+                out: torch.Tensor | None = None, seqlens: torch.Tensor | None = None, accumulate: bool = False,
+                stream=None):
+    """Attention weight each key of a prompt received, fp32 [B,Hkv,Nkv] (or the first Nkv
+    entries of the rows of ``out``, for instance a cache's weights)."""
+    B, Hq, Nq, d = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _stream_context(stream, q.device):
+        if out is None:
+            out = torch.empty((B, Hkv, Nkv), dtype=torch.float32, device=q.device)
+        ws = torch.empty(max(16, attn_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d)), dtype=torch.uint8,
+                         device=q.device)
+        attn_key_weights(q, k, lse, out, causal, scale, ws, seqlens, accumulate, stream)
+    return out

@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID_ARG", -2: "ATTN_ERR_UNSUPPOR
 
 # (name, restype, argtypes)
 _VP, _I, _F, _SZ, _ULL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_ulonglong
+_LL = ctypes.c_longlong
 SIGNATURES = [
     ("attn_status_string", ctypes.c_char_p, [_I]),
     ("attn_version", ctypes.c_char_p, []),
@@ -48,6 +49,15 @@ SIGNATURES = [
     ("attn_fp4_scores", _I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP]),
     ("attn_quantize_fp8", _I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP]),
     ("attn_fwd_fp8", _I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _F, _I, _VP]),
+    ("attn_kv4_append", _I, [_VP] * 11 + [_I] * 5 + [_VP]),
+    ("attn_kv4_read", _I, [_VP] * 4 + [_I] * 5 + [_VP]),
+    ("attn_decode_kv4_splits", _I, [_I] * 5),
+    ("attn_decode_kv4_workspace_bytes", _SZ, [_I] * 7),
+    ("attn_decode_kv4", _I, [_VP] * 9 + [_I] * 5 + [_F, _I, _VP, _SZ, _VP]),
+    ("attn_key_weights_workspace_bytes", _SZ, [_I] * 6),
+    ("attn_key_weights", _I, [_VP] * 5 + [_I] * 8 + [_F, _LL, _VP, _SZ, _VP]),
+    ("attn_kv4_evict_workspace_bytes", _SZ, [_I] * 4),
+    ("attn_kv4_evict", _I, [_VP] * 11 + [_I] * 6 + [_VP, _SZ, _VP]),
     ("attn_check_status", _I, [_VP]),
     ("attn_set_wait_limit_ns", None, [_ULL]),
     ("attn_watchdog_selftest", _I, [_ULL, _VP]),
@@ -363,6 +373,136 @@ def attn_fwd_fp8(q, qs, k, ks, v, vs, o, lse, causal: bool, scale: float, rotate
                              B, H, Nq, Nkv, d, int(bool(causal)), float(scale), int(bool(rotated)),
                              _stream(stream))
     _check("attn_fwd_fp8", rc)
+
+
+def _on_device(*ts):
+    """The device all given tensors are on, as a context that makes it the current
+    one (a launch goes to the current device, whatever memory it points at)."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _expect_kv4(B, Hkv, cap, d, **arrays):
+    """Shapes and types of a 4-bit cache's arrays (those given as codes, scales,
+    fp32 or int32 per slot, int32 per sequence)."""
+    specs = {"c": ((B, Hkv, cap, d // 2), _U8), "s": ((B, Hkv, cap, d // 32), _BF16),
+             "w": ((B, Hkv, cap), _F32), "p": ((B, Hkv, cap), _I32), "b": ((B,), _I32)}
+    for name, (kind, t) in arrays.items():
+        if t is not None:
+            _expect((t, *specs[kind], name))
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def attn_kv4_append(k, v, kc, ks, vc, vs, starts, counts=None, weights=None, positions=None, next_pos=None, stream=None):
+    """Quantise k, v [B,Hkv,n,d] bf16 and write them to slots starts[b] + i of a 4-bit
+    cache (kc, vc uint8 [B,Hkv,capacity,d/2], ks, vs bf16 [B,Hkv,capacity,d/32])."""
+    _need_cuda(k, v, kc, ks, vc, vs, starts, counts, weights, positions, next_pos)
+    B, Hkv, n, d = k.shape
+    cap = kc.shape[2]
+    _expect((k, (B, Hkv, n, d), _BF16, "k"), (v, (B, Hkv, n, d), _BF16, "v"))
+    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), starts=("b", starts),
+                counts=("b", counts), weights=("w", weights), positions=("p", positions), next_pos=("b", next_pos))
+    with _on_device(k, v, kc, ks, vc, vs, starts, counts, weights, positions, next_pos):
+        rc = load().attn_kv4_append(_ptr(k), _ptr(v), _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(starts),
+                                    _ptr(counts), _ptr(weights), _ptr(positions), _ptr(next_pos), B, Hkv, n, cap, d,
+                                    _stream(stream))
+    _check("attn_kv4_append", rc)
+
+
+def attn_kv4_read(codes, scales, out, starts=None, stream=None):
+    """Values of slots starts[b] + i (from slot 0 without starts) as bf16 [B,Hkv,n,d]."""
+    _need_cuda(codes, scales, out, starts)
+    B, Hkv, n, d = out.shape
+    cap = codes.shape[2]
+    _expect((out, (B, Hkv, n, d), _BF16, "out"))
+    _expect_kv4(B, Hkv, cap, d, codes=("c", codes), scales=("s", scales), starts=("b", starts))
+    with _on_device(codes, scales, out, starts):
+        rc = load().attn_kv4_read(_ptr(codes), _ptr(scales), _ptr(out), _ptr(starts), B, Hkv, n, cap, d,
+                                  _stream(stream))
+    _check("attn_kv4_read", rc)
+
+
+def attn_decode_kv4_splits(B: int, Hq: int, Hkv: int, capacity: int, d: int) -> int:
+    return int(load().attn_decode_kv4_splits(B, Hq, Hkv, capacity, d))
+
+
+def attn_decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, capacity: int, d: int, num_splits: int,
+                                    with_weights: bool) -> int:
+    return int(load().attn_decode_kv4_workspace_bytes(B, Hq, Hkv, capacity, d, num_splits, int(bool(with_weights))))
+
+
+def attn_decode_kv4(q, kc, ks, vc, vs, o, lse, seqlens, scale: float, num_splits: int, workspace, weights=None,
+                    stream=None):
+    """Decode over a 4-bit cache: q, o [B,Hq,1,d] bf16, lse [B,Hq,1] fp32, live slots
+    [0, seqlens[b]); weights [B,Hkv,capacity] fp32 grows by the attention weights."""
+    _need_cuda(q, kc, ks, vc, vs, o, lse, seqlens, workspace, weights)
+    B, Hq, _, d = q.shape
+    Hkv, cap = kc.shape[1], kc.shape[2]
+    _expect((q, (B, Hq, 1, d), _BF16, "q"), (o, (B, Hq, 1, d), _BF16, "o"), (lse, (B, Hq, 1), _F32, "lse"))
+    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), seqlens=("b", seqlens),
+                weights=("w", weights))
+    with _on_device(q, kc, ks, vc, vs, o, lse, seqlens, workspace, weights):
+        rc = load().attn_decode_kv4(_ptr(q), _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(o), _ptr(lse),
+                                    _ptr(weights), _ptr(seqlens), B, Hq, Hkv, cap, d, float(scale), int(num_splits),
+                                    _ptr(workspace), _nbytes(workspace), _stream(stream))
+    _check("attn_decode_kv4", rc)
+
+
+def attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nkv: int, d: int) -> int:
+    return int(load().attn_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d))
+
+
+def attn_key_weights(q, k, lse, weights, causal: bool, scale: float, workspace=None, seqlens=None,
+                     accumulate: bool = False, stream=None):
+    """Attention weight of each key of a prompt: q [B,Hq,Nq,d], k [B,Hkv,Nkv,d] bf16, lse
+    [B,Hq,Nq] (the forward's) -> the first Nkv entries of the rows of weights
+    [B,Hkv,>=Nkv] fp32."""
+    _need_cuda(q, k, lse, weights, workspace, seqlens)
+    B, Hq, Nq, d = q.shape
+    Hkv, Nkv = k.shape[1], k.shape[2]
+    if weights.dim() != 3 or weights.shape[2] < Nkv:
+        raise ValueError(f"weights: expected rows of at least {Nkv} entries, got {tuple(weights.shape)}")
+    stride = weights.shape[2]
+    _expect((q, (B, Hq, Nq, d), _BF16, "q"), (k, (B, Hkv, Nkv, d), _BF16, "k"), (lse, (B, Hq, Nq), _F32, "lse"),
+            (weights, (B, Hkv, stride), _F32, "weights"))
+    if seqlens is not None:
+        _expect((seqlens, (B,), _I32, "seqlens"))
+    with _on_device(q, k, lse, weights, workspace, seqlens):
+        rc = load().attn_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(weights), _ptr(seqlens), B, Hq, Hkv, Nq, Nkv,
+                                     d, int(bool(causal)), int(bool(accumulate)), float(scale), stride,
+                                     _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                                     _stream(stream))
+    _check("attn_key_weights", rc)
+
+
+def attn_kv4_evict_workspace_bytes(B: int, Hkv: int, capacity: int, n_keep: int) -> int:
+    return int(load().attn_kv4_evict_workspace_bytes(B, Hkv, capacity, n_keep))
+
+
+def attn_kv4_evict(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weights_out, positions_out, kept,
+                   n_recent: int, workspace, stream=None):
+    """Keep n_keep = kept.shape[2] slots of every (batch, cache head): the n_recent newest,
+    then those of the largest weight; kept int32 [B,Hkv,n_keep] gets their old slots."""
+    _need_cuda(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weights_out, positions_out, kept, workspace)
+    B, Hkv, cap = kc.shape[:3]
+    d = 2 * kc.shape[3]
+    n_keep = kept.shape[2]
+    _expect((kept, (B, Hkv, n_keep), _I32, "kept"))
+    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), weights=("w", weights),
+                positions=("p", positions), seqlens=("b", seqlens), next_pos=("b", next_pos),
+                weights_out=("w", weights_out), positions_out=("p", positions_out))
+    with _on_device(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weights_out, positions_out, kept, workspace):
+        rc = load().attn_kv4_evict(_ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(weights), _ptr(positions),
+                                   _ptr(seqlens), _ptr(next_pos), _ptr(weights_out), _ptr(positions_out), _ptr(kept),
+                                   B, Hkv, cap, d, n_keep, int(n_recent), _ptr(workspace), _nbytes(workspace),
+                                   _stream(stream))
+    _check("attn_kv4_evict", rc)
 
 
 def attn_check_status(stream=None) -> int:

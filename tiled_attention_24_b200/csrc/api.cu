@@ -20,6 +20,9 @@
 #include "bwd_bf16.cuh"
 #include "fwd_fp8.cuh"
 #include "decode_tc.cuh"
+#include "kv4.cuh"
+#include "decode_kv4.cuh"
+#include "key_weights.cuh"
 
 namespace {
 
@@ -873,6 +876,236 @@ int attn_fp4_scores(const uint8_t* q, const uint8_t* q_sf, const uint8_t* k, con
     return ATTN_ERR_MISALIGNED;
   return launch_fp4<true>(q, q_sf, k, k_sf, nullptr, k_sf, nullptr, nullptr, s, B, H, Nq, Nkv, 0, 1.f, 0,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------- 4-bit key/value cache
+// Shape checks every entry point of the 4-bit cache shares; ATTN_OK with
+// B * Hkv == 0 is for the caller to notice.
+static int kv4_shape(int B, int Hkv, int capacity, int d) {
+  if (B < 0 || Hkv < 0 || capacity < 16 || capacity % 16 != 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > 0x7fffffffLL || (long long)B * Hkv * capacity > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int attn_kv4_append(const attn_bf16_t* k, const attn_bf16_t* v, uint8_t* kc, attn_bf16_t* ks, uint8_t* vc,
+                    attn_bf16_t* vs, const int* starts, const int* counts, float* weights, int* positions,
+                    const int* next_pos, int B, int Hkv, int n, int capacity, int d, void* stream) {
+  int rc = kv4_shape(B, Hkv, capacity, d);
+  if (rc != ATTN_OK) return rc;
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Hkv == 0 || n == 0) return ATTN_OK;
+  const long long rows = (long long)B * Hkv * n;
+  if (rows > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!k || !v || !kc || !ks || !vc || !vs || !starts || (positions && !next_pos)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) ||
+      !aligned4(starts) || !aligned4(counts) || !aligned4(weights) || !aligned4(positions) || !aligned4(next_pos))
+    return ATTN_ERR_MISALIGNED;
+  ta::Kv4AppendParams p;
+  p.k = k;
+  p.v = v;
+  p.kc = kc;
+  p.vc = vc;
+  p.ks = ks;
+  p.vs = vs;
+  p.starts = starts;
+  p.counts = counts;
+  p.weights = weights;
+  p.positions = positions;
+  p.next_pos = next_pos;
+  p.Hkv = Hkv;
+  p.n = n;
+  p.cap = capacity;
+  p.rows = (unsigned)rows;
+  const unsigned grid = (unsigned)((rows + 31) / 32);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 128)
+    ta::kv4_append_kernel<4><<<grid, 256, 0, st>>>(p);
+  else
+    ta::kv4_append_kernel<2><<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn_bf16_t* out, const int* starts, int B,
+                  int Hkv, int n, int capacity, int d, void* stream) {
+  int rc = kv4_shape(B, Hkv, capacity, d);
+  if (rc != ATTN_OK) return rc;
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Hkv == 0 || n == 0) return ATTN_OK;
+  const long long rows = (long long)B * Hkv * n;
+  if (rows > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!codes || !scales || !out) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out) || !aligned4(starts)) return ATTN_ERR_MISALIGNED;
+  const unsigned grid = (unsigned)((rows + 31) / 32);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 128)
+    ta::kv4_read_kernel<4><<<grid, 256, 0, st>>>(codes, scales, out, starts, Hkv, n, capacity, (unsigned)rows);
+  else
+    ta::kv4_read_kernel<2><<<grid, 256, 0, st>>>(codes, scales, out, starts, Hkv, n, capacity, (unsigned)rows);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int attn_decode_kv4_splits(int B, int Hq, int Hkv, int capacity, int d) {
+  (void)d;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || capacity <= 0) return 1;
+  const long long heads = (long long)B * Hq;
+  const long long want = (8 * 148 + heads - 1) / heads;
+  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 1024), capacity / 128));
+}
+
+// workspace of attn_decode_kv4: partial O, partial LSE, then (with weights) the
+// scores, each part at a multiple of 256 bytes
+static size_t kv4_decode_x_offset(long long BH, int d, int S) { return (decode_ws_bytes(BH, d, S) + 255) & ~size_t(255); }
+
+size_t attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int capacity, int d, int num_splits,
+                                       int with_weights) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || num_splits <= 0 || kv4_shape(B, Hkv, capacity, d) != ATTN_OK) return 0;
+  const long long BH = (long long)B * Hq;
+  return kv4_decode_x_offset(BH, d, num_splits) + (with_weights ? (size_t)BH * capacity * sizeof(float) : 0);
+}
+
+int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* ks, const uint8_t* vc,
+                    const attn_bf16_t* vs, attn_bf16_t* o, float* lse, float* weights, const int* seqlens, int B,
+                    int Hq, int Hkv, int capacity, int d, float scale, int num_splits, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (Hq < 0 || Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
+  int rc = kv4_shape(B, Hkv, capacity, d);
+  if (rc != ATTN_OK) return rc;
+  if (num_splits < 1 || num_splits > 1024) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Hq == 0) return ATTN_OK;
+  const long long BH = (long long)B * Hq;
+  if (BH * num_splits > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (!q || !kc || !ks || !vc || !vs || !o || !lse || !seqlens || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned16(o) ||
+      !aligned4(lse) || !aligned4(weights) || !aligned4(seqlens) || !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  if (workspace_bytes < attn_decode_kv4_workspace_bytes(B, Hq, Hkv, capacity, d, num_splits, weights != nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  ta::DecKv4Params p;
+  p.q = q;
+  p.kc = kc;
+  p.vc = vc;
+  p.ks = ks;
+  p.vs = vs;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        (((size_t)BH * num_splits * d * sizeof(float) + 255) & ~size_t(255)));
+  p.x = weights ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_decode_x_offset(BH, d, num_splits))
+                : nullptr;
+  p.seqlens = seqlens;
+  p.Hq = Hq;
+  p.group = Hq / Hkv;
+  p.cap = capacity;
+  p.S = num_splits;
+  p.sl2 = scale * 1.4426950408889634f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)(BH * num_splits);
+  if (d == 128) {
+    ta::decode_kv4_kernel<4><<<grid, 128, 0, st>>>(p);
+    ta::decode_kv4_combine_kernel<128><<<(unsigned)BH, 128, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
+  } else {
+    ta::decode_kv4_kernel<2><<<grid, 128, 0, st>>>(p);
+    ta::decode_kv4_combine_kernel<64><<<(unsigned)BH, 64, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
+  }
+  if (weights) {
+    if ((long long)B * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+    ta::decode_kv4_weights_kernel<<<dim3((unsigned)((capacity + 255) / 256), (unsigned)(B * Hkv)), 256, 0, st>>>(
+        p.x, lse, weights, seqlens, Hq, Hkv, capacity);
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d) {
+  (void)B; (void)Hq; (void)Hkv; (void)Nq; (void)Nkv; (void)d;
+  return 0;
+}
+
+int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* lse, float* weights, const int* seqlens,
+                     int B, int Hq, int Hkv, int Nq, int Nkv, int d, int causal, int accumulate, float scale,
+                     long long weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || Hq < 0 || Nq < 0 || Nkv < 0 || weights_stride < Nkv) return ATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Hq == 0 || Nkv == 0) return ATTN_OK;
+  if ((long long)B * Hq > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (!k || !weights || (Nq > 0 && (!q || !lse))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned4(weights) || !aligned4(seqlens) || (Nq > 0 && (!aligned16(q) || !aligned4(lse))) ||
+      !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  const size_t need = attn_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  ta::KeyWeightsParams p;
+  p.q = q;
+  p.k = k;
+  p.lse = lse;
+  p.w = weights;
+  p.seqlens = seqlens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.Nkv = Nkv;
+  p.causal = causal ? 1 : 0;
+  p.accumulate = accumulate ? 1 : 0;
+  p.stride = weights_stride;
+  p.sl2 = scale * 1.4426950408889634f;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)((Nkv + 127) / 128), (unsigned)(B * Hkv));
+  if (d == 128)
+    ta::key_weights_kernel<128><<<grid, 128, 0, st>>>(p);
+  else
+    ta::key_weights_kernel<64><<<grid, 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_kv4_evict_workspace_bytes(int B, int Hkv, int capacity, int n_keep) {
+  if (B <= 0 || Hkv <= 0 || capacity <= 0 || n_keep <= 0) return 0;
+  return (size_t)B * Hkv * 2 * n_keep * sizeof(int);
+}
+
+int attn_kv4_evict(uint8_t* kc, attn_bf16_t* ks, uint8_t* vc, attn_bf16_t* vs, const float* weights,
+                   const int* positions, const int* seqlens, const int* next_pos, float* weights_out,
+                   int* positions_out, int* kept, int B, int Hkv, int capacity, int d, int n_keep, int n_recent,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = kv4_shape(B, Hkv, capacity, d);
+  if (rc != ATTN_OK) return rc;
+  if (n_keep < 1 || n_keep > capacity || n_recent < 0 || n_recent > n_keep) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Hkv == 0) return ATTN_OK;
+  if (!kc || !ks || !vc || !vs || !weights || !positions || !seqlens || !next_pos || !weights_out || !positions_out ||
+      !kept || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned4(weights) ||
+      !aligned4(positions) || !aligned4(seqlens) || !aligned4(next_pos) || !aligned4(weights_out) ||
+      !aligned4(positions_out) || !aligned4(kept) || !aligned16(workspace))
+    return ATTN_ERR_MISALIGNED;
+  if (workspace_bytes < attn_kv4_evict_workspace_bytes(B, Hkv, capacity, n_keep)) return ATTN_ERR_INVALID_ARG;
+  ta::Kv4EvictParams p;
+  p.kc = kc;
+  p.vc = vc;
+  p.ks = ks;
+  p.vs = vs;
+  p.weights = weights;
+  p.positions = positions;
+  p.seqlens = seqlens;
+  p.next_pos = next_pos;
+  p.weights_out = weights_out;
+  p.positions_out = positions_out;
+  p.kept = kept;
+  p.lists = static_cast<int*>(workspace);
+  p.Hkv = Hkv;
+  p.cap = capacity;
+  p.n_keep = n_keep;
+  p.n_recent = n_recent;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ta::kv4_select_kernel<<<(unsigned)(B * Hkv), ta::KV4_SEL_THREADS, 0, st>>>(p);
+  const long long rows = (long long)B * Hkv * n_keep;
+  const unsigned grid = (unsigned)((rows + 31) / 32);
+  if (d == 128)
+    ta::kv4_move_kernel<4><<<grid, 256, 0, st>>>(p, (unsigned)rows);
+  else
+    ta::kv4_move_kernel<2><<<grid, 256, 0, st>>>(p, (unsigned)rows);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 int attn_check_status(void* stream) {
