@@ -947,10 +947,20 @@ int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn_bf16_t* 
 
 int attn_decode_kv4_splits(int B, int Hq, int Hkv, int capacity, int d) {
   (void)d;
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || capacity <= 0) return 1;
-  const long long heads = (long long)B * Hq;
-  const long long want = (8 * 148 + heads - 1) / heads;
-  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 1024), capacity / 128));
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq < Hkv || capacity <= 0) return 1;
+  // two CTAs share an SM, so 296 run at once: the fewest chunks per row whose
+  // last wave is at least 95 % full, else the fullest; no chunk below 256 slots
+  const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8), wave = 2 * 148;
+  const int most = (int)std::max<long long>(1, std::min<long long>(1024, capacity / 256));
+  int best = 1;
+  double fill = 0.0;
+  for (int s = 1; s <= most; ++s) {
+    const long long n = items * s;
+    const double f = (double)n / (double)((n + wave - 1) / wave * wave);
+    if (f > fill + 1e-9) fill = f, best = s;
+    if (fill >= 0.95) break;
+  }
+  return best;
 }
 
 // workspace of attn_decode_kv4: partial O, partial LSE, then (with weights) the
@@ -994,18 +1004,22 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   p.x = weights ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_decode_x_offset(BH, d, num_splits))
                 : nullptr;
   p.seqlens = seqlens;
-  p.Hq = Hq;
+  p.Hkv = Hkv;
   p.group = Hq / Hkv;
   p.cap = capacity;
   p.S = num_splits;
+  p.blocks = (p.group + 7) / 8;
   p.sl2 = scale * 1.4426950408889634f;
+  p.timeout_ns = g_wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)(BH * num_splits);
+  const unsigned grid = (unsigned)((long long)B * Hkv * p.blocks * num_splits);
   if (d == 128) {
-    ta::decode_kv4_kernel<4><<<grid, 128, 0, st>>>(p);
+    if ((rc = set_smem_attr(ta::decode_kv4_kernel<4>, ta::DecKv4Cfg<4>::SMEM)) != ATTN_OK) return rc;
+    ta::decode_kv4_kernel<4><<<grid, 256, ta::DecKv4Cfg<4>::SMEM, st>>>(p);
     ta::decode_kv4_combine_kernel<128><<<(unsigned)BH, 128, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
   } else {
-    ta::decode_kv4_kernel<2><<<grid, 128, 0, st>>>(p);
+    if ((rc = set_smem_attr(ta::decode_kv4_kernel<2>, ta::DecKv4Cfg<2>::SMEM)) != ATTN_OK) return rc;
+    ta::decode_kv4_kernel<2><<<grid, 256, ta::DecKv4Cfg<2>::SMEM, st>>>(p);
     ta::decode_kv4_combine_kernel<64><<<(unsigned)BH, 64, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
   }
   if (weights) {
