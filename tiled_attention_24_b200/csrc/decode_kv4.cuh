@@ -50,19 +50,12 @@ struct DecKv4Cfg {
 static_assert(DecKv4Cfg<4>::WARPS * 8 * 128 * 4 <= DecKv4Cfg<4>::RING, "partial outputs reuse the ring");
 static_assert(DecKv4Cfg<2>::WARPS * 8 * 64 * 4 <= DecKv4Cfg<2>::RING, "partial outputs reuse the ring");
 
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = a b + c, f16 operands, f32 accumulation
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 // transpose of an 8x8 matrix of 16-bit elements held two per lane
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -70,36 +63,53 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+// (a & MASK) ^ flip in one logic operation
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t flip) {
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "n"(MASK), "r"(flip));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// two fp32 -> packed f16x2 (round to nearest even), `lo` in the low half
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 __device__ __forceinline__ float bf2f(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16)); }
 
-// NG words of a row's scales as floats
-__device__ __forceinline__ void kv4_scales(const uint2& w, float (&f)[4]) {
-  f[0] = bf2f(w.x, 0), f[1] = bf2f(w.x, 1), f[2] = bf2f(w.y, 0), f[3] = bf2f(w.y, 1);
-}
-__device__ __forceinline__ void kv4_scales(const uint32_t& w, float (&f)[2]) { f[0] = bf2f(w, 0), f[1] = bf2f(w, 1); }
+// word i (two groups) of a row's scales
+__device__ __forceinline__ uint32_t kv4_word(const uint2& w, int i) { return i ? w.y : w.x; }
+__device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w; }
 
 // One CTA: one block of <= 8 query heads of a cache head, one chunk of its slots.
 // Each warp walks its own tiles of 32 slots (every 8th of the chunk) through its
 // own ring of bulk copies and keeps its own running max, sum and output; the
 // warps meet once, at the end.  Per 16 slots, r = lane / 4, t = lane % 4:
 //
-//   S^T = K Q^T   m16n8k16 f16, rows = slots, columns = heads, per channel group:
-//     A is a code's offset form n = c + 8 straight in the low bits of an fp16, a
-//     subnormal of value n 2^-24 (nibbles 0 and 2 of a halfword) or 16 n 2^-24
-//     (nibbles 1 and 3, whose q carries 1/16): masking is all the conversion there
-//     is.  B is q times a power of two per head that brings its largest channel
-//     to [2^14, 2^15): exact in fp16 down to 2^-27 of that channel.  The
-//     accumulators start from -8 sum q, which takes the offset out again.
-//   O^T = V^T P^T  m16n8k16 bf16, rows = channels, columns = heads: A is c exactly
-//     (128 + n by one logic operation, minus 136), B is p times the slot's scale
-//     of the group, rounded to bf16: the one rounding of P, as in the bf16 decode
-//     (fp16 would need a common exponent for the scales of V; the offset form
-//     would cancel against a sum far larger than the result on long rows).
+// Both products run on m16n8k16 f16 with the codes as the A operand.  A code's
+// offset form n = c + 8 sits in the low bits of an fp16 and is one as it is: a
+// subnormal of value n 2^-24 (nibbles 0 and 2 of a halfword) or 16 n 2^-24
+// (nibbles 1 and 3).  Masking (with the flip of the sign bit, one logic operation)
+// is all the conversion there is; one shift serves the two upper nibbles.
+//
+//   S^T = K Q^T, rows = slots, columns = heads, one channel group at a time:
+//     B is q times a power of two per head that brings its largest channel to
+//     [2^14, 2^15), exact in fp16 down to 2^-27 of that channel; the odd
+//     nibbles' channels carry 1/16.  The accumulators start from -8 sum q, which
+//     takes the offset out again, and each group's sum is scaled in fp32.
+//   O^T = V^T P^T, rows = channels, columns = heads: B is p times the slot's scale
+//     of the group, rounded to fp16 (the one rounding of P, 2^-11), with p
+//     taken times a power of two that keeps p s below 2^15.  That power follows
+//     the largest scale met so far as the running max follows the scores, so
+//     a product counts from 2^-31 of the largest on.  The offset goes out tile by
+//     tile through a second product with the constant -8: summed up over a long
+//     row it would swamp the result.
 template <int NG>
 __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p) {
   using C = DecKv4Cfg<NG>;
@@ -195,7 +205,12 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // per head 2t, 2t + 1: reference max of y (scores before fb), threshold above which
+  // it moves, exponent M that probabilities are taken against; vref = 2^ev, bf16x2
+  float my[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY}, M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+  int ev = -100;
+  uint32_t vref = (uint32_t)((127 - 100) << 7) * 0x10001u;
+  const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
   __syncwarp();
   __syncthreads();  // the abort flag is set up
 
@@ -208,116 +223,138 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     done = i + 1;
     const uint8_t* buf = ring + st * C::STAGE;
     const int slot0 = (t0 + warp + i * C::WARPS) * C::TILE;
-#pragma unroll 1
-    for (int sub = 0; sub < C::TILE; sub += 16) {
-      const int left = len - slot0 - sub;  // live slots from here on
-      if (left <= 0) break;
-      // ---- scores of 16 slots
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        uint32_t kw[2][NG];
-        float sc[2][NG];
+    const int left = len - slot0;  // live slots from here on
+    // ---- scores of 32 slots: [16-slot half][slot r or r + 8, head 2t or 2t + 1]
+    float y[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = sub + r + 8 * h;
-          if constexpr (NG == 4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(buf + row * 64 + t * 16);
-            kw[h][0] = __byte_perm(w.x, w.z, 0x5410), kw[h][1] = __byte_perm(w.x, w.z, 0x7632);
-            kw[h][2] = __byte_perm(w.y, w.w, 0x5410), kw[h][3] = __byte_perm(w.y, w.w, 0x7632);
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(buf + row * 32 + t * 8);
-            kw[h][0] = __byte_perm(w.x, w.y, 0x5410), kw[h][1] = __byte_perm(w.x, w.y, 0x7632);
-          }
-          kv4_scales(*reinterpret_cast<const T*>(buf + 2 * C::CODES + row * NG * 2), sc[h]);
-        }
+    for (int u = 0; u < 2; ++u) {
+      uint32_t kw[2][NG];
+      T sc[2];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float s[4] = {c0[g][0], c0[g][1], c0[g][0], c0[g][1]};
-          const uint32_t a = kw[0][g], b = kw[1][g], a8 = a >> 8, b8 = b >> 8;
-          mma_f16_16816(s, (a & 0x000F000Fu) ^ 0x00080008u, (b & 0x000F000Fu) ^ 0x00080008u,
-                        (a & 0x00F000F0u) ^ 0x00800080u, (b & 0x00F000F0u) ^ 0x00800080u, qb[g][0], qb[g][1]);
-          mma_f16_16816(s, (a8 & 0x000F000Fu) ^ 0x00080008u, (b8 & 0x000F000Fu) ^ 0x00080008u,
-                        (a8 & 0x00F000F0u) ^ 0x00800080u, (b8 & 0x00F000F0u) ^ 0x00800080u, qb[g][2], qb[g][3]);
-          x[0] = fmaf(s[0], sc[0][g], x[0]);
-          x[1] = fmaf(s[1], sc[0][g], x[1]);
-          x[2] = fmaf(s[2], sc[1][g], x[2]);
-          x[3] = fmaf(s[3], sc[1][g], x[3]);
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * u + r + 8 * h;
+        if constexpr (NG == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(buf + row * 64 + t * 16);
+          kw[h][0] = __byte_perm(w.x, w.z, 0x5410), kw[h][1] = __byte_perm(w.x, w.z, 0x7632);
+          kw[h][2] = __byte_perm(w.y, w.w, 0x5410), kw[h][3] = __byte_perm(w.y, w.w, 0x7632);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(buf + row * 32 + t * 8);
+          kw[h][0] = __byte_perm(w.x, w.y, 0x5410), kw[h][1] = __byte_perm(w.x, w.y, 0x7632);
         }
+        sc[h] = *reinterpret_cast<const T*>(buf + 2 * C::CODES + row * NG * 2);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = x[e] * fa[e & 1] * fb[e & 1];
-      float sc[2][NG];
+      for (int g = 0; g < NG; ++g) {
+        float s[4];
+        const uint32_t a = kw[0][g], b = kw[1][g], a8 = a >> 8, b8 = b >> 8;
+        mma_f16_16816(s, and_xor<0x000F000Fu>(a, flip0), and_xor<0x000F000Fu>(b, flip0),
+                      and_xor<0x00F000F0u>(a, flip1), and_xor<0x00F000F0u>(b, flip1), qb[g][0], qb[g][1], c0[g][0],
+                      c0[g][1], c0[g][0], c0[g][1]);
+        mma_f16_16816(s, and_xor<0x000F000Fu>(a8, flip0), and_xor<0x000F000Fu>(b8, flip0),
+                      and_xor<0x00F000F0u>(a8, flip1), and_xor<0x00F000F0u>(b8, flip1), qb[g][2], qb[g][3], s[0], s[1],
+                      s[2], s[3]);
+        const float f0 = bf2f(kv4_word(sc[0], g >> 1), g & 1), f1 = bf2f(kv4_word(sc[1], g >> 1), g & 1);
+        y[u][0] = g ? fmaf(s[0], f0, y[u][0]) : s[0] * f0;
+        y[u][1] = g ? fmaf(s[1], f0, y[u][1]) : s[1] * f0;
+        y[u][2] = g ? fmaf(s[2], f1, y[u][2]) : s[2] * f1;
+        y[u][3] = g ? fmaf(s[3], f1, y[u][3]) : s[3] * f1;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[u][e] *= fa[e & 1];
+    }
+    T vs[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        kv4_scales(*reinterpret_cast<const T*>(buf + 2 * C::CODES + C::SCALES + (sub + r + 8 * h) * NG * 2), sc[h]);
-      if (left < 16) {  // slots behind the live ones: no score, and their scales may be anything
+        vs[u][h] = *reinterpret_cast<const T*>(buf + 2 * C::CODES + C::SCALES + (16 * u + r + 8 * h) * NG * 2);
+    if (left < C::TILE) {  // slots behind the live ones: no score, and their scales may be anything
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (r + 8 * h >= left) {
-            x[2 * h] = x[2 * h + 1] = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) sc[h][g] = 0.f;
+          if (16 * u + r + 8 * h >= left) {
+            y[u][2 * h] = y[u][2 * h + 1] = -INFINITY;
+            vs[u][h] = T{};
           }
-      }
-      if (p.x) {
+    }
+    if (p.x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (2 * t + (e & 1) < heads && r + 8 * (e >> 1) < left)
-            p.x[(bh0 + 2 * t + (e & 1)) * p.cap + slot0 + sub + r + 8 * (e >> 1)] = x[e];
-      }
-      // ---- running max, moved only when it must
-      const float h0 = fmaxf(x[0], x[2]), h1 = fmaxf(x[1], x[3]);
-      if (__any_sync(0xffffffffu, h0 > m[0] + C::TAU || h1 > m[1] + C::TAU)) {
-        float mx[2] = {h0, h1};
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int e = 0; e < 4; ++e) {
+          const int j = 16 * u + r + 8 * (e >> 1);
+          if (2 * t + (e & 1) < heads && j < left)
+            p.x[(bh0 + 2 * t + (e & 1)) * p.cap + slot0 + j] = y[u][e] * fb[e & 1];
+        }
+    }
+    // ---- references, moved only when they must
+    const float h0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+    const float h1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+    uint32_t vm = vref;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
-          mx[k] = fmaxf(mx[k], m[k]);
-          const float f = mx[k] == -INFINITY ? 1.f : ex2(m[k] - mx[k]);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) vm = max_bf16x2(vm, kv4_word(vs[u][h], w));
+    if (__any_sync(0xffffffffu, h0 > thr[0] || h1 > thr[1] || vm != vref)) {
+      uint32_t v = max(vm & 0xFFFFu, vm >> 16);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+      const int ev_new = v > (vref & 0xFFFFu) ? (int)(v >> 7) - 126 : ev;
+      float mx[2] = {h0, h1};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+        if (!(mx[k] > my[k])) mx[k] = my[k];
+        if (mx[k] != -INFINITY) {
+          const float Mn = fmaf(mx[k], fb[k], C::TAU + (float)(ev_new - 15));
+          const float f = my[k] == -INFINITY ? 0.f : ex2(M[k] - Mn);  // l and acc are 0 or NaN while my = -inf
           l[k] *= f;
 #pragma unroll
           for (int n = 0; n < 2 * NG; ++n) acc[n][k] *= f, acc[n][k + 2] *= f;
-          m[k] = mx[k];
+          my[k] = mx[k];
+          M[k] = Mn;
+          thr[k] = mx[k] + C::TAU / fb[k];
         }
       }
-      float pr[4];
+      ev = ev_new;
+      vref = (uint32_t)((127 + ev) << 7) * 0x10001u;
+    }
+    float pr[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float mm = m[e & 1];
-        pr[e] = ex2(x[e] - ((mm == -INFINITY ? 0.f : mm) + C::TAU));
-      }
-      l[0] += pr[0] + pr[2];
-      l[1] += pr[1] + pr[3];
-      // ---- values: piece r of slots 2t, 2t + 1, 2t + 8, 2t + 9
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[u][e] = ex2(fmaf(y[u][e], fb[e & 1], -M[e & 1]));
+      l[0] += pr[u][0] + pr[u][2];
+      l[1] += pr[u][1] + pr[u][3];
+    }
+    // ---- values: piece r of slots 2t, 2t + 1, 2t + 8, 2t + 9 of each half
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       T vw[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        vw[h] = *reinterpret_cast<const T*>(buf + C::CODES + (sub + 2 * t + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * 2 * NG);
+        vw[h] = *reinterpret_cast<const T*>(buf + C::CODES + (16 * u + 2 * t + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * 2 * NG);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t b0 = movmatrix_trans(pack_bf16(pr[0] * sc[0][g], pr[1] * sc[0][g]));
-        const uint32_t b1 = movmatrix_trans(pack_bf16(pr[2] * sc[1][g], pr[3] * sc[1][g]));
+        const float f0 = bf2f(kv4_word(vs[u][0], g >> 1), g & 1), f1 = bf2f(kv4_word(vs[u][1], g >> 1), g & 1);
+        const uint32_t b0 = movmatrix_trans(pack_f16(pr[u][0] * f0, pr[u][1] * f0));
+        const uint32_t b1 = movmatrix_trans(pack_f16(pr[u][2] * f1, pr[u][3] * f1));
         uint32_t a[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w0, w1;
-          if constexpr (NG == 4) {
-            w0 = g < 2 ? vw[2 * h].x : vw[2 * h].y;
-            w1 = g < 2 ? vw[2 * h + 1].x : vw[2 * h + 1].y;
-          } else {
-            w0 = vw[2 * h], w1 = vw[2 * h + 1];
-          }
-          a[h] = __byte_perm(w0, w1, (g & 1) ? 0x7632 : 0x5410);
-        }
-        uint32_t f[2][4];
-#pragma unroll
         for (int h = 0; h < 2; ++h)
+          a[h] = __byte_perm(kv4_word(vw[2 * h], g >> 1), kv4_word(vw[2 * h + 1], g >> 1), (g & 1) ? 0x7632 : 0x5410);
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-            f[h][n] = sub_bf16x2(((a[h] >> (4 * n)) & 0x000F000Fu) ^ 0x43084308u, 0x43084308u);
-        mma_bf16_16816(acc[2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0, b1);
-        mma_bf16_16816(acc[2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0, b1);
+        for (int n = 0; n < 2; ++n) {
+          float(&o)[4] = acc[2 * g + n];
+          mma_f16_16816(o, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1, o[0], o[1], o[2], o[3]);
+          const uint32_t w0 = n ? a[0] >> 8 : a[0], w1 = n ? a[1] >> 8 : a[1];
+          mma_f16_16816(o, and_xor<0x000F000Fu>(w0, flip0), and_xor<0x00F000F0u>(w0, flip1),
+                        and_xor<0x000F000Fu>(w1, flip0), and_xor<0x00F000F0u>(w1, flip1), b0, b1, o[0], o[1], o[2], o[3]);
+        }
       }
     }
     __syncwarp();
@@ -335,8 +372,8 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
   if (r == 0) {
-    ml[warp * 8 + 2 * t] = make_float2(m[0], l[0]);
-    ml[warp * 8 + 2 * t + 1] = make_float2(m[1], l[1]);
+    ml[warp * 8 + 2 * t] = make_float2(my[0] == -INFINITY ? -INFINITY : M[0], l[0]);
+    ml[warp * 8 + 2 * t + 1] = make_float2(my[1] == -INFINITY ? -INFINITY : M[1], l[1]);
   }
   __syncthreads();  // and every warp is done with its ring
   float* op = reinterpret_cast<float*>(smem);  // [warp][head][channel]
@@ -344,7 +381,8 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   for (int n = 0; n < 2 * NG; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      op[(warp * 8 + 2 * t + (e & 1)) * D + 32 * (n >> 1) + 4 * r + 2 * (n & 1) + (e >> 1)] = acc[n][e];
+      op[(warp * 8 + 2 * t + (e & 1)) * D + 32 * (n >> 1) + 4 * r + 2 * (n & 1) + (e >> 1)] =
+          acc[n][e] * ((e >> 1) ? 0x1p20f : 0x1p24f);  // odd nibbles carry 16
   __syncthreads();
   for (int i = threadIdx.x; i < heads * D; i += 256) {
     const int h = i / D, ch = i % D;
@@ -362,7 +400,7 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     const size_t part = (bh0 + h) * p.S + c;
     const bool live = t1 > t0;
     p.o_part[part * D + ch] = live ? o / tot : 0.f;
-    if (ch == 0) p.lse_part[part] = live ? ((mx == -INFINITY ? 0.f : mx) + C::TAU + log2f(tot)) * 0.69314718055994531f : -INFINITY;
+    if (ch == 0) p.lse_part[part] = live ? ((mx == -INFINITY ? 0.f : mx) + log2f(tot)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
