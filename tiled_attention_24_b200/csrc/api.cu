@@ -945,53 +945,74 @@ int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn_bf16_t* 
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Pieces the batch's slots are cut into: num_splits per cache head (and block of
+// 8 query heads), but no more than warps run at once (two CTAs of 8 on each of
+// 148 SMs) nor than there can be tiles.
+static long long kv4_pieces(int B, int Hq, int Hkv, int capacity, int num_splits) {
+  const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
+  const long long most = std::min<long long>(items * num_splits, 2LL * 148 * 8);
+  return std::min(most, items * ((capacity + ta::KV4_TILE - 1) / ta::KV4_TILE));
+}
+
 int attn_decode_kv4_splits(int B, int Hq, int Hkv, int capacity, int d) {
   (void)d;
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq < Hkv || capacity <= 0) return 1;
-  // two CTAs share an SM, so 296 run at once: the fewest chunks per row whose
-  // last wave is at least 95 % full, else the fullest; no chunk below 256 slots
-  const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8), wave = 2 * 148;
-  const int most = (int)std::max<long long>(1, std::min<long long>(1024, capacity / 256));
-  int best = 1;
-  double fill = 0.0;
-  for (int s = 1; s <= most; ++s) {
-    const long long n = items * s;
-    const double f = (double)n / (double)((n + wave - 1) / wave * wave);
-    if (f > fill + 1e-9) fill = f, best = s;
-    if (fill >= 0.95) break;
-  }
-  return best;
+  // enough for a piece per resident warp
+  const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
+  return (int)std::max<long long>(1, std::min<long long>(1024, (2LL * 148 * 8 + items - 1) / items));
 }
 
-// workspace of attn_decode_kv4: partial O, partial LSE, then (with weights) the
-// scores, each part at a multiple of 256 bytes
-static size_t kv4_decode_x_offset(long long BH, int d, int S) { return (decode_ws_bytes(BH, d, S) + 255) & ~size_t(255); }
+// workspace of attn_decode_kv4: partial outputs, their exponents and sums, then
+// (with weights) the scores, each part at a multiple of 256 bytes.  Every new
+// piece and every new item begins a partial result.
+struct Kv4DecodeWs {
+  size_t ml, x, bytes;
+};
+static Kv4DecodeWs kv4_decode_ws(int B, int Hq, int Hkv, int capacity, int d, int num_splits, bool with_weights) {
+  const int group = Hq / Hkv, blocks = (group + 7) / 8;
+  const size_t parts = ((size_t)kv4_pieces(B, Hq, Hkv, capacity, num_splits) + (size_t)B * Hkv * blocks) * std::min(8, group);
+  auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  Kv4DecodeWs w;
+  w.ml = up(parts * d * sizeof(float));
+  w.x = w.ml + up(parts * sizeof(float2));
+  w.bytes = w.x + (with_weights ? (size_t)B * Hq * capacity * sizeof(float) : 0);
+  return w;
+}
+
+static int kv4_decode_shape(int B, int Hq, int Hkv, int capacity, int d, int num_splits) {
+  if (Hq < 0 || Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
+  const int rc = kv4_shape(B, Hkv, capacity, d);
+  if (rc != ATTN_OK) return rc;
+  if (num_splits < 1 || num_splits > 1024) return ATTN_ERR_INVALID_ARG;
+  const int blocks = (Hq / Hkv + 7) / 8;
+  // tiles (and pieces and items together) are counted in 32 bits
+  if ((long long)B * Hq > 0x7fffffffLL ||
+      (long long)B * Hkv * blocks * ((capacity + ta::KV4_TILE - 1) / ta::KV4_TILE + 1) > 0x7ff00000LL)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
 
 size_t attn_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int capacity, int d, int num_splits,
                                        int with_weights) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || num_splits <= 0 || kv4_shape(B, Hkv, capacity, d) != ATTN_OK) return 0;
-  const long long BH = (long long)B * Hq;
-  return kv4_decode_x_offset(BH, d, num_splits) + (with_weights ? (size_t)BH * capacity * sizeof(float) : 0);
+  if (B <= 0 || Hq <= 0 || kv4_decode_shape(B, Hq, Hkv, capacity, d, num_splits) != ATTN_OK) return 0;
+  return kv4_decode_ws(B, Hq, Hkv, capacity, d, num_splits, with_weights != 0).bytes;
 }
 
 int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* ks, const uint8_t* vc,
                     const attn_bf16_t* vs, attn_bf16_t* o, float* lse, float* weights, const int* seqlens, int B,
                     int Hq, int Hkv, int capacity, int d, float scale, int num_splits, void* workspace,
                     size_t workspace_bytes, void* stream) {
-  if (Hq < 0 || Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
-  int rc = kv4_shape(B, Hkv, capacity, d);
+  int rc = kv4_decode_shape(B, Hq, Hkv, capacity, d, num_splits);
   if (rc != ATTN_OK) return rc;
-  if (num_splits < 1 || num_splits > 1024) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (B == 0 || Hq == 0) return ATTN_OK;
-  const long long BH = (long long)B * Hq;
-  if (BH * num_splits > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (weights && (long long)B * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
   if (!q || !kc || !ks || !vc || !vs || !o || !lse || !seqlens || !workspace) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned16(o) ||
       !aligned4(lse) || !aligned4(weights) || !aligned4(seqlens) || !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
-  if (workspace_bytes < attn_decode_kv4_workspace_bytes(B, Hq, Hkv, capacity, d, num_splits, weights != nullptr))
-    return ATTN_ERR_INVALID_ARG;
+  const Kv4DecodeWs ws = kv4_decode_ws(B, Hq, Hkv, capacity, d, num_splits, weights != nullptr);
+  if (workspace_bytes < ws.bytes) return ATTN_ERR_INVALID_ARG;
   ta::DecKv4Params p;
   p.q = q;
   p.kc = kc;
@@ -999,34 +1020,32 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   p.ks = ks;
   p.vs = vs;
   p.o_part = static_cast<float*>(workspace);
-  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        (((size_t)BH * num_splits * d * sizeof(float) + 255) & ~size_t(255)));
-  p.x = weights ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_decode_x_offset(BH, d, num_splits))
-                : nullptr;
+  p.ml_part = reinterpret_cast<float2*>(static_cast<char*>(workspace) + ws.ml);
+  p.x = weights ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.x) : nullptr;
   p.seqlens = seqlens;
+  p.B = B;
   p.Hkv = Hkv;
   p.group = Hq / Hkv;
   p.cap = capacity;
-  p.S = num_splits;
   p.blocks = (p.group + 7) / 8;
+  p.per_block = std::min(8, p.group);
+  p.pieces = (int)kv4_pieces(B, Hq, Hkv, capacity, num_splits);
   p.sl2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((long long)B * Hkv * p.blocks * num_splits);
+  const unsigned grid = (unsigned)((p.pieces + 7) / 8), rows = (unsigned)(B * Hq);
   if (d == 128) {
     if ((rc = set_smem_attr(ta::decode_kv4_kernel<4>, ta::DecKv4Cfg<4>::SMEM)) != ATTN_OK) return rc;
     ta::decode_kv4_kernel<4><<<grid, 256, ta::DecKv4Cfg<4>::SMEM, st>>>(p);
-    ta::decode_kv4_combine_kernel<128><<<(unsigned)BH, 128, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
+    ta::decode_kv4_merge_kernel<128><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
   } else {
     if ((rc = set_smem_attr(ta::decode_kv4_kernel<2>, ta::DecKv4Cfg<2>::SMEM)) != ATTN_OK) return rc;
     ta::decode_kv4_kernel<2><<<grid, 256, ta::DecKv4Cfg<2>::SMEM, st>>>(p);
-    ta::decode_kv4_combine_kernel<64><<<(unsigned)BH, 64, 0, st>>>(p.o_part, p.lse_part, o, lse, num_splits);
+    ta::decode_kv4_merge_kernel<64><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
   }
-  if (weights) {
-    if ((long long)B * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (weights)
     ta::decode_kv4_weights_kernel<<<dim3((unsigned)((capacity + 255) / 256), (unsigned)(B * Hkv)), 256, 0, st>>>(
         p.x, lse, weights, seqlens, Hq, Hkv, capacity);
-  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -6,10 +6,14 @@
 //   and, where asked for, w_j += sum over the heads of a cache head of
 //   2^(x_j - lse log2(e)), the accumulated attention weight of a slot.
 //
-// Split-KV as in decode.cuh: each chunk of slots leaves a normalised partial
-// result and its log-sum-exp, decode_kv4_combine_kernel merges them.  A weight
-// needs the log-sum-exp of the whole row, so the split kernel leaves the
-// scores x in the workspace and a last kernel turns them into weights.
+// The live slots of the whole batch, 32 at a time, form one sequence of tiles
+// (batch by batch, cache head by cache head), cut into equal pieces, one per
+// warp: however lengths are spread, every warp streams the same number of bytes.
+// A piece may begin and end inside a row; each (row, piece) leaves a partial
+// output, its sum and the exponent both are relative to, and a second kernel
+// merges a row's partials.  A weight needs the log-sum-exp of the whole row, so
+// the first kernel leaves the scores x in the workspace and a last kernel turns
+// them into weights.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -23,32 +27,46 @@ struct DecKv4Params {
   const uint16_t* q;             // [B][Hq][D] bf16
   const uint8_t *kc, *vc;        // [B][Hkv][cap][D/2]
   const uint16_t *ks, *vs;       // [B][Hkv][cap][D/32] bf16
-  float *o_part, *lse_part;      // [B*Hq][S][D], [B*Hq][S]
+  float* o_part;                 // [partial][head of the block][D]
+  float2* ml_part;               // [partial][head of the block]: exponent, sum
   float* x;                      // [B*Hq][cap] scores, or null
   const int* seqlens;            // [B]
-  int Hkv, group, cap, S;
+  int B, Hkv, group, cap;
   int blocks;                    // blocks of <= 8 query heads per cache head
+  int per_block;                 // heads of a block: min(8, group)
+  int pieces;
   float sl2;
   unsigned long long timeout_ns;
 };
 
+constexpr int KV4_TILE = 32;  // slots of a tile
+
 template <int NG>
 struct DecKv4Cfg {
   static constexpr int D = 32 * NG;
-  static constexpr int WARPS = 8, TILE = 32;          // slots per pipeline stage of a warp
+  static constexpr int WARPS = 8, TILE = KV4_TILE;
   static constexpr int STAGES = NG == 4 ? 3 : 6;
   static constexpr int CODES = TILE * D / 2, SCALES = TILE * NG * 2;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // K codes, V codes, K scales, V scales
-  static constexpr int RING = WARPS * STAGES * STAGE;
-  static constexpr int ML_OFF = RING;                 // running max and sum of each warp and head
-  static constexpr int BAR_OFF = ML_OFF + WARPS * 8 * 8;
-  static constexpr int SMEM = BAR_OFF + WARPS * STAGES * 8 + 16;
+  static constexpr int BAR_OFF = WARPS * STAGES * STAGE;
+  static constexpr int SMEM = BAR_OFF + WARPS * STAGES * 8 + WARPS * 4;
   // lazy rescale: the reference max moves when a score exceeds it by TAU (log2
   // units); probabilities are taken 2^-TAU smaller, so that none exceeds 1
   static constexpr float TAU = 8.f;
 };
-static_assert(DecKv4Cfg<4>::WARPS * 8 * 128 * 4 <= DecKv4Cfg<4>::RING, "partial outputs reuse the ring");
-static_assert(DecKv4Cfg<2>::WARPS * 8 * 64 * 4 <= DecKv4Cfg<2>::RING, "partial outputs reuse the ring");
+
+// Where a row's tiles lie in the batch's sequence of tiles.  An item is one block
+// of query heads of one cache head: item = (batch * Hkv + cache head) * blocks + block.
+__device__ __forceinline__ int kv4_tiles(const int* __restrict__ seqlens, int b, int cap) {
+  return (min(max(seqlens[b], 0), cap) + KV4_TILE - 1) / KV4_TILE;
+}
+// tiles of one item of each batch entry, summed over entries [0, n); whole warp
+__device__ __forceinline__ int kv4_tiles_before(const int* __restrict__ seqlens, int n, int cap) {
+  int s = 0;
+  for (int b = threadIdx.x & 31; b < n; b += 32) s += kv4_tiles(seqlens, b, cap);
+  return __reduce_add_sync(0xffffffffu, s);
+}
+__host__ __device__ inline int kv4_per_piece(int total, int pieces) { return max(1, (total + pieces - 1) / pieces); }
 
 // d = a b + c, f16 operands, f32 accumulation
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -87,10 +105,9 @@ __device__ __forceinline__ float bf2f(uint32_t w, int hi) { return __uint_as_flo
 __device__ __forceinline__ uint32_t kv4_word(const uint2& w, int i) { return i ? w.y : w.x; }
 __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w; }
 
-// One CTA: one block of <= 8 query heads of a cache head, one chunk of its slots.
-// Each warp walks its own tiles of 32 slots (every 8th of the chunk) through its
-// own ring of bulk copies and keeps its own running max, sum and output; the
-// warps meet once, at the end.  Per 16 slots, r = lane / 4, t = lane % 4:
+// Each warp is on its own: it walks its piece tile by tile through its own ring
+// of bulk copies, which runs ahead across the rows of the piece, and keeps its
+// own running max, sum and output.  r = lane / 4, t = lane % 4 below.
 //
 // Both products run on m16n8k16 f16 with the codes as the A operand.  A code's
 // offset form n = c + 8 sits in the low bits of an fp16 and is one as it is: a
@@ -118,40 +135,93 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
 
-  const int c = blockIdx.x % p.S;
-  const int hb = blockIdx.x / p.S;                     // (batch, cache head, block of heads)
-  const int bhk = hb / p.blocks, blk = hb - bhk * p.blocks;
-  const int heads = min(8, p.group - blk * 8);
-  const size_t bh0 = (size_t)bhk * p.group + blk * 8;  // first query head (batch * Hq + head)
-  const int len = min(max(p.seqlens[bhk / p.Hkv], 0), p.cap);
-  const int tiles = (len + C::TILE - 1) / C::TILE;
-  const int per = (tiles + p.S - 1) / p.S;             // tiles per chunk
-  const int t0 = min(c * per, tiles), t1 = min(t0 + per, tiles);
-  const int mine = max(0, (t1 - t0 - warp + C::WARPS - 1) / C::WARPS);
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF) + warp * C::STAGES;
-  int* abort_flag = reinterpret_cast<int*>(smem + C::BAR_OFF + C::WARPS * C::STAGES * 8);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::BAR_OFF + C::WARPS * C::STAGES * 8) + warp;  // the warp's own
   uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
-  const size_t row0 = (size_t)bhk * p.cap;
-  if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
+    *abort_flag = 0;
     for (int s = 0; s < C::STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  auto issue = [&](int i) {  // lane 0: tile i of this warp into stage i % STAGES
-    const int slot = (t0 + warp + i * C::WARPS) * C::TILE;
-    const uint32_t rows = (uint32_t)min(C::TILE, (len - slot + 15) & ~15);  // capacity is a multiple of 16
-    const uint32_t dst = smem_u32(ring + (i % C::STAGES) * C::STAGE), bar = smem_u32(&bars[i % C::STAGES]);
+  __syncwarp();
+
+  // ---- this warp's piece: tiles [first, first + mine) of the batch
+  const int per_entry = p.Hkv * p.blocks;  // items of a batch entry
+  const int total = kv4_tiles_before(p.seqlens, p.B, p.cap) * per_entry;
+  const int per = kv4_per_piece(total, p.pieces);
+  // 64 bits: pieces that start behind the last tile
+  const long long first = (long long)(blockIdx.x * C::WARPS + warp) * per;
+  const int mine = (int)max(0LL, min((long long)per, total - first));
+  if (mine == 0) return;
+  const int piece = blockIdx.x * C::WARPS + warp;
+  int b = 0, before = 0;  // batch entry of the first tile, tiles before it
+  for (int b0 = 0;; b0 += 32) {
+    const int n = b0 + lane < p.B ? kv4_tiles(p.seqlens, b0 + lane, p.cap) * per_entry : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned beyond = __ballot_sync(0xffffffffu, before + sum > first);
+    if (beyond) {
+      const int at = __ffs(beyond) - 1;
+      b = b0 + at;
+      before += __shfl_sync(0xffffffffu, sum - n, at);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  // a place in the batch's tiles: entry b of length len, its item, tile of tiles
+  struct Place {
+    int b, len, tiles, item, tile;
+  };
+  auto enter = [&](Place& c, int bb) {
+    c.b = bb;
+    c.len = min(max(p.seqlens[bb], 0), p.cap);
+    c.tiles = (c.len + C::TILE - 1) / C::TILE;
+  };
+  auto next_item = [&](Place& c) {  // only where there is one with tiles
+    c.tile = 0;
+    if (++c.item == (c.b + 1) * per_entry) {
+      do {
+        enter(c, c.b + 1);
+        c.item = c.b * per_entry;
+      } while (c.tiles == 0);
+    }
+  };
+  Place at, ahead;
+  enter(at, b);
+  {
+    const int rem = (int)(first - before);
+    at.item = b * per_entry + rem / at.tiles;
+    at.tile = rem % at.tiles;
+  }
+  ahead = at;
+  int issued = 0;
+  auto issue = [&]() {  // lane 0: the next tile of the piece into the next stage
+    const int slot = ahead.tile * C::TILE;
+    const uint32_t rows = (uint32_t)min(C::TILE, (ahead.len - slot + 15) & ~15);  // capacity is a multiple of 16
+    const size_t row = (size_t)(ahead.item / p.blocks) * p.cap + slot;
+    const int st = issued % C::STAGES;
+    const uint32_t dst = smem_u32(ring + st * C::STAGE), bar = smem_u32(&bars[st]);
     mbar_arrive_expect_tx(bar, rows * (D + 4 * NG));
-    bulk_load(dst, p.kc + (row0 + slot) * (D / 2), rows * (D / 2), bar);
-    bulk_load(dst + 2 * C::CODES, p.ks + (row0 + slot) * NG, rows * NG * 2, bar);
-    bulk_load(dst + C::CODES, p.vc + (row0 + slot) * (D / 2), rows * (D / 2), bar);
-    bulk_load(dst + 2 * C::CODES + C::SCALES, p.vs + (row0 + slot) * NG, rows * NG * 2, bar);
+    bulk_load(dst, p.kc + row * (D / 2), rows * (D / 2), bar);
+    bulk_load(dst + 2 * C::CODES, p.ks + row * NG, rows * NG * 2, bar);
+    bulk_load(dst + C::CODES, p.vc + row * (D / 2), rows * (D / 2), bar);
+    bulk_load(dst + 2 * C::CODES + C::SCALES, p.vs + row * NG, rows * NG * 2, bar);
+    if (++issued < mine && ++ahead.tile == ahead.tiles) next_item(ahead);
   };
   if (lane == 0)
-    for (int i = 0; i < min(mine, C::STAGES); ++i) issue(i);
+    while (issued < min(mine, C::STAGES)) issue();
 
+  bool ok = true;
+  int i = 0;  // tiles of the piece done
+  while (true) {
+    const int bhk = at.item / p.blocks, blk = at.item - bhk * p.blocks;
+    const int heads = min(8, p.group - blk * 8);
+    const size_t bh0 = (size_t)bhk * p.group + blk * 8;  // first query head (batch * Hq + head)
   // ---- queries: head r, channels 32 g + 8 t + 0..7 of each group, as B fragments
   uint32_t qb[NG][4];
   float c0[NG][2];  // accumulator start of heads 2t, 2t + 1
@@ -171,21 +241,23 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     // largest channel in [2^e, 2^(e+1)) (below the normal numbers: e = -126); a
     // head with an infinity or a NaN is left as it is, its outputs are NaN anyway
     const int e = m >= 0x7F80u ? 14 : max(1, (int)(m >> 7)) - 127;
+    const int e0 = (14 - e) / 2;  // 2^(14 - e) in two factors
+    const float up0 = __uint_as_float((uint32_t)(127 + e0) << 23), up1 = __uint_as_float((uint32_t)(127 + 14 - e - e0) << 23);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint32_t ww[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
       float f[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = ldexpf(bf2f(ww[i], 0), 14 - e);
-        f[2 * i + 1] = ldexpf(bf2f(ww[i], 1), 14 - e) * 0.0625f;
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = bf2f(ww[k], 0) * up0 * up1;
+        f[2 * k + 1] = bf2f(ww[k], 1) * up0 * (up1 * 0.0625f);
       }
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // nibble i of the two halfwords: channels i and 4 + i
-        const __half2 h = __floats2half2_rn(f[i], f[4 + i]);
-        qb[g][i] = *reinterpret_cast<const uint32_t*>(&h);
-        sum += (__low2float(h) + __high2float(h)) * ((i & 1) ? 16.f : 1.f);
+      for (int k = 0; k < 4; ++k) {  // nibble k of the two halfwords: channels k and 4 + k
+        const __half2 h = __floats2half2_rn(f[k], f[4 + k]);
+        qb[g][k] = *reinterpret_cast<const uint32_t*>(&h);
+        sum += (__low2float(h) + __high2float(h)) * ((k & 1) ? 16.f : 1.f);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -195,9 +267,10 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     }
     // x = score * sl2 * 2^(24 + e - 14), the power of two in two factors
     const int eh = (e + 10) / 2;
-    const float a = ldexpf(1.f, eh), b = ldexpf(p.sl2, e + 10 - eh);
-    fa[0] = __shfl_sync(0xffffffffu, a, 8 * t), fa[1] = __shfl_sync(0xffffffffu, a, 8 * t + 4);
-    fb[0] = __shfl_sync(0xffffffffu, b, 8 * t), fb[1] = __shfl_sync(0xffffffffu, b, 8 * t + 4);
+    const float fae = __uint_as_float((uint32_t)(127 + eh) << 23);
+    const float fbe = p.sl2 * __uint_as_float((uint32_t)(127 + e + 10 - eh) << 23);
+    fa[0] = __shfl_sync(0xffffffffu, fae, 8 * t), fa[1] = __shfl_sync(0xffffffffu, fae, 8 * t + 4);
+    fb[0] = __shfl_sync(0xffffffffu, fbe, 8 * t), fb[1] = __shfl_sync(0xffffffffu, fbe, 8 * t + 4);
   }
 
   float acc[2 * NG][4];
@@ -211,19 +284,14 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   int ev = -100;
   uint32_t vref = (uint32_t)((127 - 100) << 7) * 0x10001u;
   const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
-  __syncwarp();
-  __syncthreads();  // the abort flag is set up
 
-  bool ok = true;
-  int done = 0;
-  for (int i = 0; i < mine; ++i) {
+  for (const int end = min(mine, i + at.tiles - at.tile); i < end; ++i, ++at.tile) {
     const int st = i % C::STAGES;
     ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars[st]), (i / C::STAGES) & 1, abort_flag, p.timeout_ns));
     if (!ok) break;
-    done = i + 1;
     const uint8_t* buf = ring + st * C::STAGE;
-    const int slot0 = (t0 + warp + i * C::WARPS) * C::TILE;
-    const int left = len - slot0;  // live slots from here on
+    const int slot0 = at.tile * C::TILE;
+    const int left = at.len - slot0;  // live slots from here on
     // ---- scores of 32 slots: [16-slot half][slot r or r + 8, head 2t or 2t + 1]
     float y[2][4];
 #pragma unroll
@@ -358,74 +426,94 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
       }
     }
     __syncwarp();
-    if (lane == 0 && i + C::STAGES < mine) issue(i + C::STAGES);
+    if (lane == 0 && issued < mine) issue();
   }
-  if (!ok) {  // never leave a copy in flight
-    for (int i = done; i < min(mine, done + C::STAGES); ++i)
-      wait_bar_drain(smem_u32(&bars[i % C::STAGES]), (i / C::STAGES) & 1, p.timeout_ns);
-  }
+  if (!ok) break;
 
-  // ---- the warps' results meet: max, sums and outputs through shared memory
+  // ---- the row's partial result of this piece
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
-  float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
-  if (r == 0) {
-    ml[warp * 8 + 2 * t] = make_float2(my[0] == -INFINITY ? -INFINITY : M[0], l[0]);
-    ml[warp * 8 + 2 * t + 1] = make_float2(my[1] == -INFINITY ? -INFINITY : M[1], l[1]);
+  const size_t part = (size_t)(piece + at.item) * p.per_block;  // unique: the next piece or item has the next number
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (2 * t + k >= heads) continue;
+    float* o = p.o_part + (part + 2 * t + k) * D + 4 * r;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)  // odd nibbles carry 16
+      *reinterpret_cast<float4*>(o + 32 * g) = make_float4(acc[2 * g][k] * 0x1p24f, acc[2 * g][k + 2] * 0x1p20f,
+                                                           acc[2 * g + 1][k] * 0x1p24f, acc[2 * g + 1][k + 2] * 0x1p20f);
+    if (r == 0) p.ml_part[part + 2 * t + k] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
   }
-  __syncthreads();  // and every warp is done with its ring
-  float* op = reinterpret_cast<float*>(smem);  // [warp][head][channel]
-#pragma unroll
-  for (int n = 0; n < 2 * NG; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      op[(warp * 8 + 2 * t + (e & 1)) * D + 32 * (n >> 1) + 4 * r + 2 * (n & 1) + (e >> 1)] =
-          acc[n][e] * ((e >> 1) ? 0x1p20f : 0x1p24f);  // odd nibbles carry 16
-  __syncthreads();
-  for (int i = threadIdx.x; i < heads * D; i += 256) {
-    const int h = i / D, ch = i % D;
-    float mx = -INFINITY, tot = 0.f, o = 0.f;
-#pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) mx = fmaxf(mx, ml[w * 8 + h].x);
-#pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) {
-      const float2 v = ml[w * 8 + h];
-      // a warp without slots has sum 0; one whose scores are all NaN has no max but a NaN sum
-      const float f = v.x == mx ? 1.f : ex2(v.x - mx);
-      tot = fmaf(v.y, f, tot);
-      o = fmaf(op[(w * 8 + h) * D + ch], f, o);
-    }
-    const size_t part = (bh0 + h) * p.S + c;
-    const bool live = t1 > t0;
-    p.o_part[part * D + ch] = live ? o / tot : 0.f;
-    if (ch == 0) p.lse_part[part] = live ? ((mx == -INFINITY ? 0.f : mx) + log2f(tot)) * 0.69314718055994531f : -INFINITY;
+  if (i == mine) break;
+  next_item(at);
+  }
+  if (!ok) {  // never leave a copy in flight
+    issued = __shfl_sync(0xffffffffu, issued, 0);
+    for (; i < issued; ++i) wait_bar_drain(smem_u32(&bars[i % C::STAGES]), (i / C::STAGES) & 1, p.timeout_ns);
   }
 }
 
-// Merge of a row's chunks: LSE = log sum_c exp(LSE_c), O = sum_c exp(LSE_c - LSE) O_c.
-// A chunk without slots has LSE_c = -inf; a NaN in a live slot stays a NaN.
+// Merge of a row's partials, one CTA per (batch, query head): with f = 2^(M_c - max M),
+// O = sum f O_c / sum f l_c, LSE = ln 2 (max M + log2 sum f l_c).  A row without
+// slots has no partial; a NaN in a live slot stays one.
+constexpr int KV4_MERGE_THREADS = 256;
 template <int D>
-__global__ void __launch_bounds__(D)
-    decode_kv4_combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                              uint16_t* __restrict__ o, float* __restrict__ lse, int S) {
-  const int bh = blockIdx.x, e = threadIdx.x;
-  const float* lp = lse_part + (size_t)bh * S;
+__global__ void __launch_bounds__(KV4_MERGE_THREADS)
+    decode_kv4_merge_kernel(const DecKv4Params p, uint16_t* __restrict__ o, float* __restrict__ lse) {
+  constexpr int LANES = D / 4, GROUPS = KV4_MERGE_THREADS / LANES;  // float4 of channels; partials side by side
+  __shared__ float s_max[KV4_MERGE_THREADS / 32];
+  __shared__ float4 s_o[GROUPS][LANES];
+  __shared__ float s_l[GROUPS];
+  const int Hq = p.Hkv * p.group, b = blockIdx.x / Hq, h = blockIdx.x % Hq;
+  const int tiles = kv4_tiles(p.seqlens, b, p.cap);
+  const int lane4 = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  uint16_t* orow = o + (size_t)blockIdx.x * D;
+  if (tiles == 0) {
+    if (threadIdx.x < LANES) *reinterpret_cast<uint2*>(orow + 4 * lane4) = make_uint2(0, 0);
+    if (threadIdx.x == 0) lse[blockIdx.x] = -INFINITY;
+    return;
+  }
+  const int per_entry = p.Hkv * p.blocks;
+  const int total = kv4_tiles_before(p.seqlens, p.B, p.cap) * per_entry;
+  const int per = kv4_per_piece(total, p.pieces);
+  const int in_entry = h / p.group * p.blocks + h % p.group / 8, head = h % p.group % 8;
+  const int item = b * per_entry + in_entry;
+  const int t0 = kv4_tiles_before(p.seqlens, b, p.cap) * per_entry + in_entry * tiles;
+  const int c0 = t0 / per, n = (t0 + tiles - 1) / per - c0 + 1;  // pieces the row lies in
+  const size_t part = (size_t)(c0 + item) * p.per_block + head;
+  const float2* ml = p.ml_part + part;
   float mx = -INFINITY;
-  bool any = false;
-  for (int c = 0; c < S; ++c) {
-    any |= !(lp[c] == -INFINITY);
-    mx = fmaxf(mx, lp[c]);
+  for (int c = threadIdx.x; c < n; c += KV4_MERGE_THREADS) mx = fmaxf(mx, ml[(size_t)c * p.per_block].x);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < KV4_MERGE_THREADS / 32; ++k) mx = fmaxf(mx, s_max[k]);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int c = grp; c < n; c += GROUPS) {
+    const float2 v = ml[(size_t)c * p.per_block];
+    const float4 w = reinterpret_cast<const float4*>(p.o_part + (part + (size_t)c * p.per_block) * D)[lane4];
+    const float f = v.x == mx ? 1.f : ex2(v.x - mx);  // all NaN: no max, but NaN sums
+    l = fmaf(f, v.y, l);
+    a.x = fmaf(f, w.x, a.x), a.y = fmaf(f, w.y, a.y), a.z = fmaf(f, w.z, a.z), a.w = fmaf(f, w.w, a.w);
   }
-  float tot = 0.f, acc = 0.f;
-  for (int c = 0; any && c < S; ++c) {
-    const float w = ex2((lp[c] - mx) * 1.4426950408889634f);
-    tot += w;
-    acc = fmaf(w, o_part[((size_t)bh * S + c) * D + e], acc);
+  s_o[grp][lane4] = a;
+  if (lane4 == 0) s_l[grp] = l;
+  __syncthreads();
+  if (threadIdx.x >= LANES) return;
+  for (int k = 1; k < GROUPS; ++k) {
+    const float4 w = s_o[k][lane4];
+    a.x += w.x, a.y += w.y, a.z += w.z, a.w += w.w;
+    l += s_l[k];
   }
-  o[(size_t)bh * D + e] = (uint16_t)(pack_bf16(any ? acc / tot : 0.f, 0.f) & 0xFFFFu);
-  if (e == 0) lse[bh] = any ? mx + logf(tot) : -INFINITY;
+  const float inv = 1.f / l;
+  *reinterpret_cast<uint2*>(orow + 4 * lane4) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (threadIdx.x == 0) lse[blockIdx.x] = ((mx == -INFINITY ? 0.f : mx) + log2f(l)) * 0.69314718055994531f;
 }
 
 // w_j += sum_h 2^(x_hj - lse_h log2 e) over the query heads of one cache head
