@@ -946,11 +946,11 @@ int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn_bf16_t* 
 }
 
 // Pieces the batch's slots are cut into: num_splits per cache head (and block of
-// 8 query heads), but no more than warps run at once (two CTAs of 8 on each of
-// 148 SMs) nor than there can be tiles.
+// 8 query heads), but no more than warps run at once nor than there can be tiles.
+constexpr long long kKv4Warps = 148LL * ta::KV4_CTAS * ta::KV4_WARPS;
 static long long kv4_pieces(int B, int Hq, int Hkv, int capacity, int num_splits) {
   const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
-  const long long most = std::min<long long>(items * num_splits, 2LL * 148 * 8);
+  const long long most = std::min<long long>(items * num_splits, kKv4Warps);
   return std::min(most, items * ((capacity + ta::KV4_TILE - 1) / ta::KV4_TILE));
 }
 
@@ -959,7 +959,7 @@ int attn_decode_kv4_splits(int B, int Hq, int Hkv, int capacity, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq < Hkv || capacity <= 0) return 1;
   // enough for a piece per resident warp
   const long long items = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
-  return (int)std::max<long long>(1, std::min<long long>(1024, (2LL * 148 * 8 + items - 1) / items));
+  return (int)std::max<long long>(1, std::min<long long>(1024, (kKv4Warps + items - 1) / items));
 }
 
 // workspace of attn_decode_kv4: partial outputs, their exponents and sums, then
@@ -1033,14 +1033,14 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   p.sl2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((p.pieces + 7) / 8), rows = (unsigned)(B * Hq);
+  const unsigned grid = (unsigned)((p.pieces + ta::KV4_WARPS - 1) / ta::KV4_WARPS), rows = (unsigned)(B * Hq);
   if (d == 128) {
     if ((rc = set_smem_attr(ta::decode_kv4_kernel<4>, ta::DecKv4Cfg<4>::SMEM)) != ATTN_OK) return rc;
-    ta::decode_kv4_kernel<4><<<grid, 256, ta::DecKv4Cfg<4>::SMEM, st>>>(p);
+    ta::decode_kv4_kernel<4><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<4>::SMEM, st>>>(p);
     ta::decode_kv4_merge_kernel<128><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
   } else {
     if ((rc = set_smem_attr(ta::decode_kv4_kernel<2>, ta::DecKv4Cfg<2>::SMEM)) != ATTN_OK) return rc;
-    ta::decode_kv4_kernel<2><<<grid, 256, ta::DecKv4Cfg<2>::SMEM, st>>>(p);
+    ta::decode_kv4_kernel<2><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<2>::SMEM, st>>>(p);
     ta::decode_kv4_merge_kernel<64><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
   }
   if (weights)

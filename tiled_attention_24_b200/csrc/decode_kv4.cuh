@@ -39,13 +39,14 @@ struct DecKv4Params {
   unsigned long long timeout_ns;
 };
 
-constexpr int KV4_TILE = 32;  // slots of a tile
+constexpr int KV4_TILE = 32;                // slots of a tile
+constexpr int KV4_WARPS = 4, KV4_CTAS = 3;  // warps of a CTA, CTAs of an SM
 
 template <int NG>
 struct DecKv4Cfg {
   static constexpr int D = 32 * NG;
-  static constexpr int WARPS = 8, TILE = KV4_TILE;
-  static constexpr int STAGES = NG == 4 ? 3 : 6;
+  static constexpr int WARPS = KV4_WARPS, CTAS = KV4_CTAS, TILE = KV4_TILE;
+  static constexpr int STAGES = NG == 4 ? 4 : 8;
   static constexpr int CODES = TILE * D / 2, SCALES = TILE * NG * 2;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // K codes, V codes, K scales, V scales
   static constexpr int BAR_OFF = WARPS * STAGES * STAGE;
@@ -128,7 +129,7 @@ __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w;
 //     tile through a second product with the constant -8: summed up over a long
 //     row it would swamp the result.
 template <int NG>
-__global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p) {
+__global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS) decode_kv4_kernel(const DecKv4Params p) {
   using C = DecKv4Cfg<NG>;
   using T = typename Kv4Piece<NG>::T;
   constexpr int D = C::D;
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   // a place in the batch's tiles: entry b of length len, its item, tile of tiles
   struct Place {
     int b, len, tiles, item, tile;
+    size_t row;  // first slot of the item's cache head
   };
   auto enter = [&](Place& c, int bb) {
     c.b = bb;
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
         c.item = c.b * per_entry;
       } while (c.tiles == 0);
     }
+    c.row = (size_t)(c.item / p.blocks) * p.cap;
   };
   Place at, ahead;
   enter(at, b);
@@ -197,15 +200,15 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     const int rem = (int)(first - before);
     at.item = b * per_entry + rem / at.tiles;
     at.tile = rem % at.tiles;
+    at.row = (size_t)(at.item / p.blocks) * p.cap;
   }
   ahead = at;
   int issued = 0;
-  auto issue = [&]() {  // lane 0: the next tile of the piece into the next stage
+  auto issue = [&](int stage) {  // lane 0: the next tile of the piece into the next stage
     const int slot = ahead.tile * C::TILE;
     const uint32_t rows = (uint32_t)min(C::TILE, (ahead.len - slot + 15) & ~15);  // capacity is a multiple of 16
-    const size_t row = (size_t)(ahead.item / p.blocks) * p.cap + slot;
-    const int st = issued % C::STAGES;
-    const uint32_t dst = smem_u32(ring + st * C::STAGE), bar = smem_u32(&bars[st]);
+    const size_t row = ahead.row + slot;
+    const uint32_t dst = smem_u32(ring + stage * C::STAGE), bar = smem_u32(&bars[stage]);
     mbar_arrive_expect_tx(bar, rows * (D + 4 * NG));
     bulk_load(dst, p.kc + row * (D / 2), rows * (D / 2), bar);
     bulk_load(dst + 2 * C::CODES, p.ks + row * NG, rows * NG * 2, bar);
@@ -214,17 +217,19 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
     if (++issued < mine && ++ahead.tile == ahead.tiles) next_item(ahead);
   };
   if (lane == 0)
-    while (issued < min(mine, C::STAGES)) issue();
+    while (issued < min(mine, C::STAGES)) issue(issued);
 
   bool ok = true;
-  int i = 0;  // tiles of the piece done
+  int i = 0;  // tiles of the piece done; the next one's stage and its phase
+  int st = 0;
+  uint32_t phase = 0;
   while (true) {
     const int bhk = at.item / p.blocks, blk = at.item - bhk * p.blocks;
     const int heads = min(8, p.group - blk * 8);
     const size_t bh0 = (size_t)bhk * p.group + blk * 8;  // first query head (batch * Hq + head)
   // ---- queries: head r, channels 32 g + 8 t + 0..7 of each group, as B fragments
   uint32_t qb[NG][4];
-  float c0[NG][2];  // accumulator start of heads 2t, 2t + 1
+  float c0[NG][4];  // accumulator start of heads 2t, 2t + 1, once for each slot of the lane
   float fa[2], fb[2];
   {
     uint4 w[NG];
@@ -264,6 +269,10 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
       sum *= -8.f * 0x1p-24f;
       c0[g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
       c0[g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+      c0[g][2] = c0[g][0], c0[g][3] = c0[g][1];
+      // the instruction takes four registers in a row: four values of their own,
+      // or every product would start with four moves
+      asm volatile("" : "+f"(c0[g][0]), "+f"(c0[g][1]), "+f"(c0[g][2]), "+f"(c0[g][3]));
     }
     // x = score * sl2 * 2^(24 + e - 14), the power of two in two factors
     const int eh = (e + 10) / 2;
@@ -286,8 +295,7 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
   const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
 
   for (const int end = min(mine, i + at.tiles - at.tile); i < end; ++i, ++at.tile) {
-    const int st = i % C::STAGES;
-    ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars[st]), (i / C::STAGES) & 1, abort_flag, p.timeout_ns));
+    ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars[st]), phase, abort_flag, p.timeout_ns));
     if (!ok) break;
     const uint8_t* buf = ring + st * C::STAGE;
     const int slot0 = at.tile * C::TILE;
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
         const uint32_t a = kw[0][g], b = kw[1][g], a8 = a >> 8, b8 = b >> 8;
         mma_f16_16816(s, and_xor<0x000F000Fu>(a, flip0), and_xor<0x000F000Fu>(b, flip0),
                       and_xor<0x00F000F0u>(a, flip1), and_xor<0x00F000F0u>(b, flip1), qb[g][0], qb[g][1], c0[g][0],
-                      c0[g][1], c0[g][0], c0[g][1]);
+                      c0[g][1], c0[g][2], c0[g][3]);
         mma_f16_16816(s, and_xor<0x000F000Fu>(a8, flip0), and_xor<0x000F000Fu>(b8, flip0),
                       and_xor<0x00F000F0u>(a8, flip1), and_xor<0x00F000F0u>(b8, flip1), qb[g][2], qb[g][3], s[0], s[1],
                       s[2], s[3]);
@@ -426,7 +434,8 @@ __global__ void __launch_bounds__(256, 2) decode_kv4_kernel(const DecKv4Params p
       }
     }
     __syncwarp();
-    if (lane == 0 && issued < mine) issue();
+    if (lane == 0 && issued < mine) issue(st);
+    if (++st == C::STAGES) st = 0, phase ^= 1u;
   }
   if (!ok) break;
 
