@@ -6,7 +6,7 @@
 //   and, where asked for, w_j += sum over the heads of a cache head of
 //   2^(x_j - lse log2(e)), the accumulated attention weight of a slot.
 //
-// The live slots of the whole batch, 32 at a time, form one sequence of tiles
+// The live slots of the whole batch, 64 at a time, form one sequence of tiles
 // (batch by batch, cache head by cache head), cut into equal pieces, one per
 // warp: however lengths are spread, every warp streams the same number of bytes.
 // A piece may begin and end inside a row; each (row, piece) leaves a partial
@@ -39,14 +39,20 @@ struct DecKv4Params {
   unsigned long long timeout_ns;
 };
 
-constexpr int KV4_TILE = 32;                // slots of a tile
-constexpr int KV4_WARPS = 4, KV4_CTAS = 3;  // warps of a CTA, CTAs of an SM
+// A tile of 64 slots is one straight run of instructions: with 2 warps on each
+// scheduler and up to 255 registers the independent chains of its four 16-slot
+// parts hide the latencies better than more warps do with shorter runs (64
+// sequences of 8192 slots, 8 cache heads of 4 query heads, 605 MB: 148 us; 12 warps
+// of 168 registers and 32 slots 161; 16 warps of 128 and 32 slots 159; 16 slots
+// at a time 169 to 178).
+constexpr int KV4_TILE = 64;                // slots of a tile
+constexpr int KV4_WARPS = 4, KV4_CTAS = 2;  // warps of a CTA, CTAs of an SM
 
 template <int NG>
 struct DecKv4Cfg {
   static constexpr int D = 32 * NG;
   static constexpr int WARPS = KV4_WARPS, CTAS = KV4_CTAS, TILE = KV4_TILE;
-  static constexpr int STAGES = NG == 4 ? 4 : 8;
+  static constexpr int U = TILE / 16, STAGES = NG == 4 ? 2 : 4;
   static constexpr int CODES = TILE * D / 2, SCALES = TILE * NG * 2;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // K codes, V codes, K scales, V scales
   static constexpr int BAR_OFF = WARPS * STAGES * STAGE;
@@ -81,6 +87,13 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// d += a b
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // (a & MASK) ^ flip in one logic operation
 template <uint32_t MASK>
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   // ---- queries: head r, channels 32 g + 8 t + 0..7 of each group, as B fragments
   uint32_t qb[NG][4];
   float c0[NG][4];  // accumulator start of heads 2t, 2t + 1, once for each slot of the lane
-  float fa[2], fb[2];
+  float fx[2];
   {
     uint4 w[NG];
     uint32_t m = 0;
@@ -274,12 +287,10 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
       // or every product would start with four moves
       asm volatile("" : "+f"(c0[g][0]), "+f"(c0[g][1]), "+f"(c0[g][2]), "+f"(c0[g][3]));
     }
-    // x = score * sl2 * 2^(24 + e - 14), the power of two in two factors
-    const int eh = (e + 10) / 2;
-    const float fae = __uint_as_float((uint32_t)(127 + eh) << 23);
-    const float fbe = p.sl2 * __uint_as_float((uint32_t)(127 + e + 10 - eh) << 23);
-    fa[0] = __shfl_sync(0xffffffffu, fae, 8 * t), fa[1] = __shfl_sync(0xffffffffu, fae, 8 * t + 4);
-    fb[0] = __shfl_sync(0xffffffffu, fbe, 8 * t), fb[1] = __shfl_sync(0xffffffffu, fbe, 8 * t + 4);
+    // x = score * sl2 * 2^(24 + e - 14); infinite (and the outputs NaN) only for
+    // queries beyond 2^112
+    const float f = p.sl2 * __uint_as_float((uint32_t)min(254, 127 + 10 + e) << 23);
+    fx[0] = __shfl_sync(0xffffffffu, f, 8 * t), fx[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
   }
 
   float acc[2 * NG][4];
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-  // per head 2t, 2t + 1: reference max of y (scores before fb), threshold above which
+  // per head 2t, 2t + 1: reference max of y (scores before fx), threshold above which
   // it moves, exponent M that probabilities are taken against; vref = 2^ev, bf16x2
   float my[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY}, M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
   int ev = -100;
@@ -300,10 +311,11 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     const uint8_t* buf = ring + st * C::STAGE;
     const int slot0 = at.tile * C::TILE;
     const int left = at.len - slot0;  // live slots from here on
-    // ---- scores of 32 slots: [16-slot half][slot r or r + 8, head 2t or 2t + 1]
-    float y[2][4];
+    const uint8_t* ksb = buf + 2 * C::CODES;
+    // ---- scores: [16-slot part][slot r or r + 8, head 2t or 2t + 1]
+    float y[C::U][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < C::U; ++u) {
       uint32_t kw[2][NG];
       T sc[2];
 #pragma unroll
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
           const uint2 w = *reinterpret_cast<const uint2*>(buf + row * 32 + t * 8);
           kw[h][0] = __byte_perm(w.x, w.y, 0x5410), kw[h][1] = __byte_perm(w.x, w.y, 0x7632);
         }
-        sc[h] = *reinterpret_cast<const T*>(buf + 2 * C::CODES + row * NG * 2);
+        sc[h] = *reinterpret_cast<const T*>(ksb + row * NG * 2);
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -327,26 +339,23 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
                       and_xor<0x00F000F0u>(a, flip1), and_xor<0x00F000F0u>(b, flip1), qb[g][0], qb[g][1], c0[g][0],
                       c0[g][1], c0[g][2], c0[g][3]);
         mma_f16_16816(s, and_xor<0x000F000Fu>(a8, flip0), and_xor<0x000F000Fu>(b8, flip0),
-                      and_xor<0x00F000F0u>(a8, flip1), and_xor<0x00F000F0u>(b8, flip1), qb[g][2], qb[g][3], s[0], s[1],
-                      s[2], s[3]);
+                      and_xor<0x00F000F0u>(a8, flip1), and_xor<0x00F000F0u>(b8, flip1), qb[g][2], qb[g][3]);
         const float f0 = bf2f(kv4_word(sc[0], g >> 1), g & 1), f1 = bf2f(kv4_word(sc[1], g >> 1), g & 1);
         y[u][0] = g ? fmaf(s[0], f0, y[u][0]) : s[0] * f0;
         y[u][1] = g ? fmaf(s[1], f0, y[u][1]) : s[1] * f0;
         y[u][2] = g ? fmaf(s[2], f1, y[u][2]) : s[2] * f1;
         y[u][3] = g ? fmaf(s[3], f1, y[u][3]) : s[3] * f1;
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[u][e] *= fa[e & 1];
     }
-    T vs[2][2];
+    T vs[C::U][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < C::U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        vs[u][h] = *reinterpret_cast<const T*>(buf + 2 * C::CODES + C::SCALES + (16 * u + r + 8 * h) * NG * 2);
+        vs[u][h] = *reinterpret_cast<const T*>(ksb + C::SCALES + (16 * u + r + 8 * h) * NG * 2);
     if (left < C::TILE) {  // slots behind the live ones: no score, and their scales may be anything
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < C::U; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (16 * u + r + 8 * h >= left) {
@@ -356,20 +365,21 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     }
     if (p.x) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < C::U; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 16 * u + r + 8 * (e >> 1);
           if (2 * t + (e & 1) < heads && j < left)
-            p.x[(bh0 + 2 * t + (e & 1)) * p.cap + slot0 + j] = y[u][e] * fb[e & 1];
+            p.x[(bh0 + 2 * t + (e & 1)) * p.cap + slot0 + j] = y[u][e] * fx[e & 1];
         }
     }
     // ---- references, moved only when they must
-    const float h0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-    const float h1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+    float h0 = fmaxf(y[0][0], y[0][2]), h1 = fmaxf(y[0][1], y[0][3]);
+#pragma unroll
+    for (int u = 1; u < C::U; ++u) h0 = fmax3(h0, y[u][0], y[u][2]), h1 = fmax3(h1, y[u][1], y[u][3]);
     uint32_t vm = vref;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < C::U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -386,30 +396,30 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
         if (!(mx[k] > my[k])) mx[k] = my[k];
         if (mx[k] != -INFINITY) {
-          const float Mn = fmaf(mx[k], fb[k], C::TAU + (float)(ev_new - 15));
+          const float Mn = fmaf(mx[k], fx[k], C::TAU + (float)(ev_new - 15));
           const float f = my[k] == -INFINITY ? 0.f : ex2(M[k] - Mn);  // l and acc are 0 or NaN while my = -inf
           l[k] *= f;
 #pragma unroll
           for (int n = 0; n < 2 * NG; ++n) acc[n][k] *= f, acc[n][k + 2] *= f;
           my[k] = mx[k];
           M[k] = Mn;
-          thr[k] = mx[k] + C::TAU / fb[k];
+          thr[k] = mx[k] + C::TAU / fx[k];
         }
       }
       ev = ev_new;
       vref = (uint32_t)((127 + ev) << 7) * 0x10001u;
     }
-    float pr[2][4];
+    float pr[C::U][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < C::U; ++u) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[u][e] = ex2(fmaf(y[u][e], fb[e & 1], -M[e & 1]));
+      for (int e = 0; e < 4; ++e) pr[u][e] = ex2(fmaf(y[u][e], fx[e & 1], -M[e & 1]));
       l[0] += pr[u][0] + pr[u][2];
       l[1] += pr[u][1] + pr[u][3];
     }
     // ---- values: piece r of slots 2t, 2t + 1, 2t + 8, 2t + 9 of each half
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < C::U; ++u) {
       T vw[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
@@ -426,10 +436,10 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           float(&o)[4] = acc[2 * g + n];
-          mma_f16_16816(o, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1, o[0], o[1], o[2], o[3]);
+          mma_f16_16816(o, 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, b0, b1);
           const uint32_t w0 = n ? a[0] >> 8 : a[0], w1 = n ? a[1] >> 8 : a[1];
           mma_f16_16816(o, and_xor<0x000F000Fu>(w0, flip0), and_xor<0x00F000F0u>(w0, flip1),
-                        and_xor<0x000F000Fu>(w1, flip0), and_xor<0x00F000F0u>(w1, flip1), b0, b1, o[0], o[1], o[2], o[3]);
+                        and_xor<0x000F000Fu>(w1, flip0), and_xor<0x00F000F0u>(w1, flip1), b0, b1);
         }
       }
     }
