@@ -401,6 +401,21 @@ static int launch_decode_tc(const void* q, const void* k, const void* v, float* 
   }
 }
 
+template <int D>
+static int launch_key_weights(const void* q, const void* k, int B, int Hq, int Hkv, int Nq, int Nkv,
+                              const ta::KeyWeightsParams& p, cudaStream_t st) {
+  using C = ta::KeyWCfg<D>;
+  CUtensorMap tq, tk;
+  int rc;
+  if ((rc = make_tmap_rows(&tq, q, D, (long long)B * Hq * Nq, 128)) != ATTN_OK) return rc;
+  if ((rc = make_tmap_bf16(&tk, k, D, Nkv, B * Hkv)) != ATTN_OK) return rc;
+  if ((rc = set_smem_attr(ta::key_weights_kernel<D>, C::SMEM)) != ATTN_OK) return rc;
+  const long long grid = (long long)p.BHkv * p.key_tiles * p.parts;
+  if (grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  ta::key_weights_kernel<D><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(tq, tk, p);
+  return ATTN_OK;
+}
+
 extern "C" {
 
 const char* attn_status_string(int s) {
@@ -1049,46 +1064,74 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Parts the query tiles of a key tile are cut into: enough CTAs (two on each of
+// 148 SMs) for about four rounds of them, so that the shorter ones of a causal
+// prompt fill the gaps the longer leave, but at least 8 query tiles a part.
+static int key_weights_parts(int B, int Hq, int Hkv, int Nq, int Nkv) {
+  const long long ctas = (long long)B * Hkv * ((Nkv + 127) / 128), q_tiles = ((long long)(Hq / Hkv) * Nq + 127) / 128;
+  const long long want = (4LL * 2 * 148 + ctas - 1) / ctas;
+  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 64), q_tiles / 8));
+}
+
+static int key_weights_shape(int B, int Hq, int Hkv, int Nq, int Nkv, int d) {
+  if (B < 0 || Hq < 0 || Nq < 0 || Nkv < 0) return ATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  // rows of q and their tiles are counted in 32 bits, heads in a grid dimension
+  if ((long long)B * Hkv > 65535 || (long long)B * Hq * Nq > 0x7fffff00LL || (long long)B * Hkv * Nkv > 0x7fffff00LL)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 size_t attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d) {
-  (void)B; (void)Hq; (void)Hkv; (void)Nq; (void)Nkv; (void)d;
-  return 0;
+  if (B <= 0 || Hq <= 0 || Nq <= 0 || Nkv <= 0 || key_weights_shape(B, Hq, Hkv, Nq, Nkv, d) != ATTN_OK) return 0;
+  const int parts = key_weights_parts(B, Hq, Hkv, Nq, Nkv);
+  return parts > 1 ? (size_t)parts * B * Hkv * Nkv * sizeof(float) : 0;
 }
 
 int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* lse, float* weights, const int* seqlens,
                      int B, int Hq, int Hkv, int Nq, int Nkv, int d, int causal, int accumulate, float scale,
                      long long weights_stride, void* workspace, size_t workspace_bytes, void* stream) {
-  if (B < 0 || Hq < 0 || Nq < 0 || Nkv < 0 || weights_stride < Nkv) return ATTN_ERR_INVALID_ARG;
-  if (Hkv < 1 || (Hq > 0 && (Hq % Hkv != 0 || Hkv > Hq))) return ATTN_ERR_INVALID_ARG;
+  int rc = key_weights_shape(B, Hq, Hkv, Nq, Nkv, d);
+  if (rc != ATTN_OK) return rc;
+  if (weights_stride < Nkv) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (B == 0 || Hq == 0 || Nkv == 0) return ATTN_OK;
-  if ((long long)B * Hq > 65535) return ATTN_ERR_UNSUPPORTED;
   if (!k || !weights || (Nq > 0 && (!q || !lse))) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned4(weights) || !aligned4(seqlens) || (Nq > 0 && (!aligned16(q) || !aligned4(lse))) ||
       !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
   const size_t need = attn_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 columns((unsigned)((Nkv + 255) / 256), (unsigned)(B * Hkv));
+  if (Nq == 0) {
+    if (!accumulate) ta::key_weights_none_kernel<<<columns, 256, 0, st>>>(weights, weights_stride, Nkv);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
   ta::KeyWeightsParams p;
-  p.q = q;
-  p.k = k;
   p.lse = lse;
   p.w = weights;
+  p.parts_out = static_cast<float*>(workspace);
   p.seqlens = seqlens;
-  p.Hq = Hq;
+  p.BHkv = B * Hkv;
   p.Hkv = Hkv;
+  p.group = Hq / Hkv;
   p.Nq = Nq;
   p.Nkv = Nkv;
   p.causal = causal ? 1 : 0;
   p.accumulate = accumulate ? 1 : 0;
+  p.key_tiles = (Nkv + 127) / 128;
+  p.q_tiles = (int)(((long long)p.group * Nq + 127) / 128);
+  p.parts = key_weights_parts(B, Hq, Hkv, Nq, Nkv);
+  p.per_part = (p.q_tiles + p.parts - 1) / p.parts;
   p.stride = weights_stride;
   p.sl2 = scale * 1.4426950408889634f;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)((Nkv + 127) / 128), (unsigned)(B * Hkv));
-  if (d == 128)
-    ta::key_weights_kernel<128><<<grid, 128, 0, st>>>(p);
-  else
-    ta::key_weights_kernel<64><<<grid, 128, 0, st>>>(p);
+  p.timeout_ns = g_wait_ns;
+  rc = d == 128 ? launch_key_weights<128>(q, k, B, Hq, Hkv, Nq, Nkv, p, st)
+                : launch_key_weights<64>(q, k, B, Hq, Hkv, Nq, Nkv, p, st);
+  if (rc != ATTN_OK) return rc;
+  if (p.parts > 1) ta::key_weights_join_kernel<<<columns, 256, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
