@@ -410,9 +410,7 @@ static int launch_key_weights(const void* q, const void* k, int B, int Hq, int H
   if ((rc = make_tmap_rows(&tq, q, D, (long long)B * Hq * Nq, 128)) != ATTN_OK) return rc;
   if ((rc = make_tmap_bf16(&tk, k, D, Nkv, B * Hkv)) != ATTN_OK) return rc;
   if ((rc = set_smem_attr(ta::key_weights_kernel<D>, C::SMEM)) != ATTN_OK) return rc;
-  const long long grid = (long long)p.BHkv * p.key_tiles * p.parts;
-  if (grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  ta::key_weights_kernel<D><<<(unsigned)grid, C::THREADS, C::SMEM, st>>>(tq, tk, p);
+  ta::key_weights_kernel<D><<<(unsigned)std::min(p.items, 148), C::THREADS, C::SMEM, st>>>(tq, tk, p);
   return ATTN_OK;
 }
 
@@ -1064,12 +1062,12 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Parts the query tiles of a key tile are cut into: enough CTAs (two on each of
-// 148 SMs) for about four rounds of them, so that the shorter ones of a causal
-// prompt fill the gaps the longer leave, but at least 8 query tiles a part.
+// Parts the query tiles of a pair of key tiles are cut into: about 8 items for
+// each of 148 SMs, so that the uneven items of a causal prompt even out, but at
+// least 8 query tiles a part (an item's start and end cost about one).
 static int key_weights_parts(int B, int Hq, int Hkv, int Nq, int Nkv) {
-  const long long ctas = (long long)B * Hkv * ((Nkv + 127) / 128), q_tiles = ((long long)(Hq / Hkv) * Nq + 127) / 128;
-  const long long want = (4LL * 2 * 148 + ctas - 1) / ctas;
+  const long long pairs = (long long)B * Hkv * ((Nkv + 255) / 256), q_tiles = ((long long)(Hq / Hkv) * Nq + 127) / 128;
+  const long long want = (8LL * 148 + pairs - 1) / pairs;
   return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 64), q_tiles / 8));
 }
 
@@ -1121,10 +1119,11 @@ int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* ls
   p.Nkv = Nkv;
   p.causal = causal ? 1 : 0;
   p.accumulate = accumulate ? 1 : 0;
-  p.key_tiles = (Nkv + 127) / 128;
   p.q_tiles = (int)(((long long)p.group * Nq + 127) / 128);
   p.parts = key_weights_parts(B, Hq, Hkv, Nq, Nkv);
-  p.per_part = (p.q_tiles + p.parts - 1) / p.parts;
+  const long long items = (long long)p.BHkv * ((Nkv + 255) / 256) * p.parts;
+  if (items > 0x7fff0000LL) return ATTN_ERR_UNSUPPORTED;
+  p.items = (int)items;
   p.stride = weights_stride;
   p.sl2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_wait_ns;

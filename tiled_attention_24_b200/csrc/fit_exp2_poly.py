@@ -1,4 +1,5 @@
-"""Fit the cubic used for 2^f on the FMA pipes and write exp2_poly.cuh.
+"""Fit the polynomials used for 2^f on the FMA pipes and write exp2_poly.cuh (the
+cubic of the forward) and exp2_poly5.cuh (degree 5, for sums kept in fp32).
 
     python tiled_attention_24_b200/csrc/fit_exp2_poly.py
 
@@ -76,6 +77,29 @@ def main():
         for k in range(4):
             fh.write(f"constexpr float kExp2C{k} = {float(c32[k]).hex()}f;  // {float(c32[k]):.9g}\n")
         fh.write(f"constexpr float kExp2PolyRelErr = {rel:.6e}f;\n")
+        fh.write("}  // namespace ta\n")
+    print(out, c32, rel)
+    write_degree5()
+
+
+def write_degree5():
+    """Degree 5: as accurate as the hardware exponential (2 ulp), for the weights of a
+    prompt's keys, whose probabilities are summed in fp32 and never rounded."""
+    c32 = np.array(remez(deg=5), dtype=np.float32)
+    f = np.linspace(LO, HI, 100001).astype(np.float32).astype(np.float64)
+    p = np.full_like(f, float(c32[5])).astype(np.float32)
+    for k in range(4, -1, -1):
+        p = (p.astype(np.float64) * f + float(c32[k])).astype(np.float32)
+    rel = np.abs(p.astype(np.float64) / 2.0 ** f - 1.0).max()
+    out = os.path.join(os.path.dirname(os.path.abspath(__file__)), "exp2_poly5.cuh")
+    with open(out, "w") as fh:
+        fh.write("// Generated by fit_exp2_poly.py (minimax degree 5 for 2^f, f in [-1/2, 1/2],\n")
+        fh.write(f"// relative error {rel:.3e} after rounding to fp32).  Do not edit by hand.\n")
+        fh.write("#pragma once\n")
+        fh.write("namespace ta {\n")
+        for k in range(6):
+            fh.write(f"constexpr float kExp2P5C{k} = {float(c32[k]).hex()}f;  // {float(c32[k]):.9g}\n")
+        fh.write(f"constexpr float kExp2Poly5RelErr = {rel:.6e}f;\n")
         fh.write("}  // namespace ta\n")
     print(out, c32, rel)
 
