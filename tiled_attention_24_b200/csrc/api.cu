@@ -414,6 +414,37 @@ static int launch_key_weights(const void* q, const void* k, int B, int Hq, int H
   return ATTN_OK;
 }
 
+// One cluster per (batch, cache head): a CTA for every 4096 slots of the
+// capacity, up to 8 (128 heads of 32768 slots: 8 CTAs each, two on an SM).
+template <int NG>
+static int launch_kv4_evict(const ta::Kv4EvictParams& p, int heads, cudaStream_t st) {
+  int cl = 1;
+  while (cl < 8 && p.cap > 4096 * cl) cl *= 2;
+  if ((long long)heads * cl > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  const int per = (p.cap + cl - 1) / cl;
+  const int slice = (per + ta::KV4_EVICT_THREADS - 1) / ta::KV4_EVICT_THREADS * ta::KV4_EVICT_THREADS;
+  const bool cached = slice <= ta::KV4_EVICT_CACHED;
+  const size_t smem = sizeof(ta::Kv4EvictShared) + (size_t)slice / 8 + (cached ? (size_t)slice * 4 : 0);
+  if (smem > 200 * 1024) return ATTN_ERR_UNSUPPORTED;  // more than 12 million slots
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(heads * cl));
+  cfg.blockDim = dim3(ta::KV4_EVICT_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cl;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int rc = cached ? set_smem_attr(ta::kv4_evict_kernel<NG, true>, (int)smem)
+                        : set_smem_attr(ta::kv4_evict_kernel<NG, false>, (int)smem);
+  if (rc != ATTN_OK) return rc;
+  const cudaError_t e = cached ? cudaLaunchKernelEx(&cfg, ta::kv4_evict_kernel<NG, true>, p)
+                               : cudaLaunchKernelEx(&cfg, ta::kv4_evict_kernel<NG, false>, p);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 extern "C" {
 
 const char* attn_status_string(int s) {
@@ -1173,13 +1204,8 @@ int attn_kv4_evict(uint8_t* kc, attn_bf16_t* ks, uint8_t* vc, attn_bf16_t* vs, c
   p.n_keep = n_keep;
   p.n_recent = n_recent;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  ta::kv4_select_kernel<<<(unsigned)(B * Hkv), ta::KV4_SEL_THREADS, 0, st>>>(p);
-  const long long rows = (long long)B * Hkv * n_keep;
-  const unsigned grid = (unsigned)((rows + 31) / 32);
-  if (d == 128)
-    ta::kv4_move_kernel<4><<<grid, 256, 0, st>>>(p, (unsigned)rows);
-  else
-    ta::kv4_move_kernel<2><<<grid, 256, 0, st>>>(p, (unsigned)rows);
+  rc = d == 128 ? launch_kv4_evict<4>(p, B * Hkv, st) : launch_kv4_evict<2>(p, B * Hkv, st);
+  if (rc != ATTN_OK) return rc;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -18,6 +18,8 @@
 // instructions need each lane to hold the same groups in the same registers;
 // in channel order one lane's 16 bytes would be one whole group.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "ptx.cuh"
 
 namespace ta {
@@ -192,113 +194,228 @@ __device__ __forceinline__ uint32_t kv4_rank_key(float w, int pos, long long fir
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Which slots of one (batch, cache head) stay, one CTA each.  The n_keep-th
-// largest key is found digit by digit; then one ordered walk gives every slot
-// its place: kept slots below n_keep stay, the r-th kept slot at or beyond
-// n_keep goes into the r-th hole below it.
-constexpr int KV4_SEL_THREADS = 1024;
-__global__ void __launch_bounds__(KV4_SEL_THREADS) kv4_select_kernel(const Kv4EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int wsum[2][32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
-  const int bh = blockIdx.x, b = bh / p.Hkv;
-  const int L = min(max(p.seqlens[b], 0), p.cap);
-  int* kept = p.kept + (size_t)bh * p.n_keep;
-  if (L <= p.n_keep) {
-    for (int j = threadIdx.x; j < p.n_keep; j += KV4_SEL_THREADS) kept[j] = j < L ? j : -1;
-    return;
-  }
-  const float* w = p.weights + (size_t)bh * p.cap;
-  const int* pos = p.positions + (size_t)bh * p.cap;
-  const long long first_recent = (long long)p.next_pos[b] - p.n_recent;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The whole eviction of one (batch, cache head) by one cluster of up to 8 CTAs,
+// each with a contiguous slice of the slots, keys kept in shared memory:
+//   1. the n_keep-th largest key, 11 + 11 + 10 bits at a time: histograms per CTA,
+//      added up in the first CTA's shared memory, which finds the digit;
+//   2. keys above it stay, and as many equal ones as are wanted, lowest slots first
+//      (ranks by ballots, prefix sums over warps and CTAs);
+//   3. the lists of holes (below n_keep, not kept) and sources (kept, at or beyond
+//      n_keep), both in slot order, and the r-th source moves into the r-th hole.
+// Rows move from slots >= n_keep into slots < n_keep only, so no row is read after
+// it was overwritten and a repeated call moves the same rows again.
+constexpr int KV4_EVICT_THREADS = 512, KV4_EVICT_WARPS = KV4_EVICT_THREADS / 32;
+constexpr int KV4_EVICT_CACHED = 16384;  // keys a CTA keeps; longer slices are ranked from memory each time
+constexpr int KV4_EVICT_BINS = 2048;
 
-  uint32_t prefix = 0, mask = 0;
-  int need = p.n_keep;  // how many of the keys that match the prefix are kept
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < L; j += KV4_SEL_THREADS) {
-      const uint32_t key = kv4_rank_key(w[j], pos[j], first_recent);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int above = 0, d = 255;
-      while (d > 0 && above + hist[d] < need) above += hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = need - above;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    mask |= 255u << shift;
-  }
+struct Kv4EvictShared {
+  int hist[KV4_EVICT_BINS];   // this CTA's
+  int total[KV4_EVICT_BINS];  // the cluster's, in its first CTA
+  int warp[2][KV4_EVICT_WARPS];
+  int cta[3][8];              // per CTA: equal keys, holes, sources
+  uint32_t prefix;
+  int need;
+};
 
-  int* holes = p.lists + (size_t)bh * 2 * p.n_keep;
-  int* sources = holes + p.n_keep;
-  int eq_before = 0, holes_before = 0, sources_before = 0;
-  // exclusive rank of this thread's flag in the CTA, and the CTA's count
-  auto scan = [&](bool f, int which, int& total) {
-    const unsigned m = __ballot_sync(0xffffffffu, f);
-    if (lane == 0) wsum[which][warp] = __popc(m);
-    __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) before += wsum[which][i];
-      total += wsum[which][i];
-    }
-    return before + __popc(m & ((1u << lane) - 1u));
-  };
-  for (int j0 = 0; j0 < L; j0 += KV4_SEL_THREADS) {
-    const int j = j0 + threadIdx.x;
-    const bool in = j < L;
-    const uint32_t key = in ? kv4_rank_key(w[j], pos[j], first_recent) : 0u;
-    int n_eq, n_other;
-    const bool eq = in && key == prefix;
-    const int r = eq_before + scan(eq, 0, n_eq);
-    const bool keep = in && (key > prefix || (eq && r < need));
-    const bool front = j < p.n_keep;
-    const bool hole = in && front && !keep, source = in && !front && keep;
-    if (front && keep) kept[j] = j;
-    __syncthreads();
-    // a chunk may hold both kinds: holes first
-    const int hr = holes_before + scan(hole, 1, n_other);
-    if (hole) holes[hr] = j;
-    holes_before += n_other;
-    __syncthreads();
-    const int sr = sources_before + scan(source, 0, n_other);
-    if (source) sources[sr] = j;
-    sources_before += n_other;
-    eq_before += n_eq;
-    __syncthreads();
-  }
-  for (int r = threadIdx.x; r < holes_before; r += KV4_SEL_THREADS) kept[holes[r]] = sources[r];
-}
-
-// Rows move from slots >= n_keep into slots < n_keep only, so no row is read
-// after it was overwritten and a repeated call moves the same rows again.
-template <int NG>
-__global__ void __launch_bounds__(256) kv4_move_kernel(const Kv4EvictParams p, unsigned rows) {
+template <int NG, bool CACHED>
+__global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4EvictParams p) {
+  namespace cg = cooperative_groups;
   constexpr int D = 32 * NG;
   using T = typename Kv4Piece<NG>::T;
-  const unsigned row = blockIdx.x * 32u + (threadIdx.x >> 3);
-  const int u = threadIdx.x & 7;
-  if (row >= rows) return;
-  const unsigned bh = row / (unsigned)p.n_keep;
-  const int j = (int)(row - bh * (unsigned)p.n_keep);
-  const int from = p.kept[row];
-  if (from < 0) return;
-  const size_t src = (size_t)bh * p.cap + from, dst = (size_t)bh * p.cap + j;
-  if (u == 0) p.weights_out[dst] = p.weights[src];
-  if (u == 1) p.positions_out[dst] = p.positions[src];
-  if (from == j) return;
-  reinterpret_cast<T*>(p.kc + dst * (D / 2))[u] = reinterpret_cast<const T*>(p.kc + src * (D / 2))[u];
-  reinterpret_cast<T*>(p.vc + dst * (D / 2))[u] = reinterpret_cast<const T*>(p.vc + src * (D / 2))[u];
-  if (u == 2) *reinterpret_cast<T*>(p.ks + dst * NG) = *reinterpret_cast<const T*>(p.ks + src * NG);
-  if (u == 3) *reinterpret_cast<T*>(p.vs + dst * NG) = *reinterpret_cast<const T*>(p.vs + src * NG);
+  extern __shared__ __align__(16) uint8_t smem[];
+  Kv4EvictShared& sh = *reinterpret_cast<Kv4EvictShared*>(smem);
+  uint32_t* keep_bits = reinterpret_cast<uint32_t*>(smem + sizeof(Kv4EvictShared));  // one bit a slot of the slice
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), CL = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bh = blockIdx.x / CL, b = bh / p.Hkv;
+  const int L = min(max(p.seqlens[b], 0), p.cap);
+  int* kept = p.kept + (size_t)bh * p.n_keep;
+  const size_t row0 = (size_t)bh * p.cap;
+  const float* w = p.weights + row0;
+  const int* pos = p.positions + row0;
+  float* w_out = p.weights_out + row0;
+  int* pos_out = p.positions_out + row0;
+  if (L <= p.n_keep) {  // nothing to evict
+    for (int j = rank * KV4_EVICT_THREADS + tid; j < p.n_keep; j += CL * KV4_EVICT_THREADS) {
+      kept[j] = j < L ? j : -1;
+      if (j < L) w_out[j] = w[j], pos_out[j] = pos[j];
+    }
+    return;
+  }
+  const long long first_recent = (long long)p.next_pos[b] - p.n_recent;
+  // this CTA's slots [j0, j0 + n), a warp's a contiguous run of them
+  const int slice = ((L + CL - 1) / CL + KV4_EVICT_THREADS - 1) / KV4_EVICT_THREADS * KV4_EVICT_THREADS;
+  const int j0 = min(rank * slice, L), n = min(slice, L - j0);
+  uint32_t* keys = keep_bits + slice / 32;
+  auto key_at = [&](int i) -> uint32_t {
+    return CACHED ? keys[i] : kv4_rank_key(w[j0 + i], pos[j0 + i], first_recent);
+  };
+  if (CACHED) {
+    for (int i = tid; i < n; i += KV4_EVICT_THREADS) keys[i] = kv4_rank_key(w[j0 + i], pos[j0 + i], first_recent);
+  }
+  for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) sh.hist[i] = sh.total[i] = 0;
+  cluster.sync();
+
+  // ---- 1. the threshold
+  uint32_t prefix = 0, mask = 0;
+  int need = p.n_keep;  // how many of the keys that match the prefix are kept
+  for (int d = 0; d < 3; ++d) {
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+    const uint32_t digits = d == 2 ? 1023u : 2047u;
+    for (int i = tid; i < n; i += KV4_EVICT_THREADS) {
+      const uint32_t key = key_at(i);
+      if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & digits], 1);
+    }
+    __syncthreads();
+    int* total = cluster.map_shared_rank(sh.total, 0);
+    for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) {
+      const int c = sh.hist[i];
+      if (c) {
+        atomicAdd(&total[i], c);
+        sh.hist[i] = 0;
+      }
+    }
+    cluster.sync();
+    if (rank == 0) {
+      // bins from the top, four to a thread: the one in which the need-th key lies
+      constexpr int PER = KV4_EVICT_BINS / KV4_EVICT_THREADS;
+      int c[PER], sum = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int bin = KV4_EVICT_BINS - 1 - (tid * PER + k);
+        c[k] = sh.total[bin];
+        sh.total[bin] = 0;
+        sum += c[k];
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (lane == 31) sh.warp[0][warp] = before;
+      __syncthreads();
+      for (int k = 0; k < warp; ++k) before += sh.warp[0][k];
+      before -= sum;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        if (before < need && need <= before + c[k]) {
+          const uint32_t found = prefix | ((uint32_t)(KV4_EVICT_BINS - 1 - (tid * PER + k)) << shift);
+          for (int r = 0; r < CL; ++r) {
+            *cluster.map_shared_rank(&sh.prefix, r) = found;
+            *cluster.map_shared_rank(&sh.need, r) = need - before;
+          }
+        }
+        before += c[k];
+      }
+    }
+    cluster.sync();
+    prefix = sh.prefix;
+    need = sh.need;
+    mask |= digits << shift;
+  }
+
+  // ---- 2. who stays
+  const int run = slice / KV4_EVICT_WARPS, i0 = warp * run, i1 = min(i0 + run, n);
+  // sums over lower warps and CTAs of a per-warp count (lane 0's); the cluster's total
+  auto before_me = [&](int count, int which, int& total) {
+    if (lane == 0) sh.warp[which & 1][warp] = count;
+    __syncthreads();
+    int before = 0, mine = 0;
+    for (int k = 0; k < KV4_EVICT_WARPS; ++k) {
+      if (k < warp) before += sh.warp[which & 1][k];
+      mine += sh.warp[which & 1][k];
+    }
+    if (tid < CL) cluster.map_shared_rank(&sh.cta[which][0], tid)[rank] = mine;
+    cluster.sync();
+    total = 0;
+    for (int r = 0; r < CL; ++r) {
+      if (r < rank) before += sh.cta[which][r];
+      total += sh.cta[which][r];
+    }
+    return before;
+  };
+  int count = 0, all;
+  for (int i = i0; i < i1; i += 32)
+    count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && key_at(i + lane) == prefix));
+  int eq = before_me(count, 0, all);
+  int holes = 0, sources = 0;
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const uint32_t key = in ? key_at(i + lane) : 0u;
+    const unsigned same = __ballot_sync(0xffffffffu, in && key == prefix);
+    const bool stays = in && (key > prefix || (key == prefix && eq + __popc(same & ((1u << lane) - 1u)) < need));
+    const unsigned keep = __ballot_sync(0xffffffffu, stays);
+    eq += __popc(same);
+    if (lane == 0) keep_bits[i / 32] = keep;
+    const int j = j0 + i + lane;
+    holes += __popc(__ballot_sync(0xffffffffu, in && !stays && j < p.n_keep));
+    sources += __popc(__ballot_sync(0xffffffffu, stays && j >= p.n_keep));
+  }
+  int moves;
+  holes = before_me(holes, 1, moves);
+  sources = before_me(sources, 2, all);
+
+  // ---- 3. the lists, then the rows
+  int* hole_list = p.lists + (size_t)bh * 2 * p.n_keep;
+  int* source_list = hole_list + p.n_keep;
+  for (int i = i0; i < i1; i += 32) {
+    const unsigned keep = keep_bits[i / 32], below = (1u << lane) - 1u;
+    const int j = j0 + i + lane;
+    const bool in = i + lane < i1, stays = (keep >> lane) & 1u, front = j < p.n_keep;
+    const unsigned h = __ballot_sync(0xffffffffu, in && !stays && front);
+    const unsigned s = __ballot_sync(0xffffffffu, in && stays && !front);
+    if ((h >> lane) & 1u) hole_list[holes + __popc(h & below)] = j;
+    if ((s >> lane) & 1u) source_list[sources + __popc(s & below)] = j;
+    holes += __popc(h);
+    sources += __popc(s);
+    if (in && stays && front) {
+      kept[j] = j;
+      if (w_out != w) w_out[j] = w[j];
+      if (pos_out != pos) pos_out[j] = pos[j];
+    }
+  }
+  cluster.sync();  // the lists are complete, and nobody reads weights or positions below n_keep any more
+  constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 4;  // 16 bytes of codes a lane
+  const int sub = lane % LANES;
+  for (int m0 = (rank * KV4_EVICT_WARPS + warp) * ROWS * DEEP; m0 < moves; m0 += CL * KV4_EVICT_WARPS * ROWS * DEEP) {
+    uint4 kc[DEEP], vc[DEEP];
+    T sc[DEEP];
+    uint32_t side[DEEP];
+    int to[DEEP], from[DEEP];
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) {
+      const int m = m0 + k * ROWS + lane / LANES;
+      to[k] = m < moves ? __ldcg(hole_list + m) : -1;
+      from[k] = m < moves ? __ldcg(source_list + m) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k)
+      if (to[k] >= 0) {
+        const size_t src = row0 + from[k];
+        kc[k] = reinterpret_cast<const uint4*>(p.kc + src * (D / 2))[sub];
+        vc[k] = reinterpret_cast<const uint4*>(p.vc + src * (D / 2))[sub];
+        if (sub < 2) {
+          sc[k] = *reinterpret_cast<const T*>((sub ? p.vs : p.ks) + src * NG);
+          side[k] = sub ? (uint32_t)pos[from[k]] : __float_as_uint(w[from[k]]);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k)
+      if (to[k] >= 0) {
+        const size_t dst = row0 + to[k];
+        reinterpret_cast<uint4*>(p.kc + dst * (D / 2))[sub] = kc[k];
+        reinterpret_cast<uint4*>(p.vc + dst * (D / 2))[sub] = vc[k];
+        if (sub < 2) {
+          *reinterpret_cast<T*>((sub ? p.vs : p.ks) + dst * NG) = sc[k];
+          if (sub)
+            pos_out[to[k]] = (int)side[k];
+          else
+            w_out[to[k]] = __uint_as_float(side[k]), kept[to[k]] = from[k];
+        }
+      }
+  }
 }
 
 }  // namespace ta
