@@ -414,12 +414,13 @@ static int launch_key_weights(const void* q, const void* k, int B, int Hq, int H
   return ATTN_OK;
 }
 
-// One cluster per (batch, cache head): a CTA for every 4096 slots of the
-// capacity, up to 8 (128 heads of 32768 slots: 8 CTAs each, two on an SM).
+// One cluster per (batch, cache head), of 1 to 8 CTAs: as many as fill the 296 that
+// run at once (two on an SM) with slices of at least 2048 slots, and no fewer
+// than keep a slice's keys in shared memory.
 template <int NG>
 static int launch_kv4_evict(const ta::Kv4EvictParams& p, int heads, cudaStream_t st) {
   int cl = 1;
-  while (cl < 8 && p.cap > 4096 * cl) cl *= 2;
+  while (cl < 8 && ((p.cap > 2048 * cl && (long long)heads * cl * 2 <= 296) || p.cap > ta::KV4_EVICT_CACHED * cl)) cl *= 2;
   if ((long long)heads * cl > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   const int per = (p.cap + cl - 1) / cl;
   const int slice = (per + ta::KV4_EVICT_THREADS - 1) / ta::KV4_EVICT_THREADS * ta::KV4_EVICT_THREADS;

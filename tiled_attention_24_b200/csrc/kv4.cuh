@@ -214,11 +214,11 @@ struct Kv4EvictShared {
   int warp[2][KV4_EVICT_WARPS];
   int cta[3][8];              // per CTA: equal keys, holes, sources
   uint32_t prefix;
-  int need;
+  int need, ties;  // of the keys that match the prefix: to be kept, in all
 };
 
 template <int NG, bool CACHED>
-__global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4EvictParams p) {
+__global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const Kv4EvictParams p) {
   namespace cg = cooperative_groups;
   constexpr int D = 32 * NG;
   using T = typename Kv4Piece<NG>::T;
@@ -251,8 +251,22 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
   auto key_at = [&](int i) -> uint32_t {
     return CACHED ? keys[i] : kv4_rank_key(w[j0 + i], pos[j0 + i], first_recent);
   };
-  if (CACHED) {
-    for (int i = tid; i < n; i += KV4_EVICT_THREADS) keys[i] = kv4_rank_key(w[j0 + i], pos[j0 + i], first_recent);
+  if (CACHED) {  // 8 slots a thread in flight
+    for (int i = tid; i < n; i += 8 * KV4_EVICT_THREADS) {
+      float a[8];
+      int c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = i + k * KV4_EVICT_THREADS;
+        a[k] = at < n ? w[j0 + at] : 0.f;
+        c[k] = at < n ? pos[j0 + at] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = i + k * KV4_EVICT_THREADS;
+        if (at < n) keys[at] = kv4_rank_key(a[k], c[k], first_recent);
+      }
+    }
   }
   for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) sh.hist[i] = sh.total[i] = 0;
   cluster.sync();
@@ -263,6 +277,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     const uint32_t digits = d == 2 ? 1023u : 2047u;
+#pragma unroll 4
     for (int i = tid; i < n; i += KV4_EVICT_THREADS) {
       const uint32_t key = key_at(i);
       if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & digits], 1);
@@ -305,6 +320,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
           for (int r = 0; r < CL; ++r) {
             *cluster.map_shared_rank(&sh.prefix, r) = found;
             *cluster.map_shared_rank(&sh.need, r) = need - before;
+            *cluster.map_shared_rank(&sh.ties, r) = c[k];
           }
         }
         before += c[k];
@@ -336,11 +352,17 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
     }
     return before;
   };
-  int count = 0, all;
-  for (int i = i0; i < i1; i += 32)
-    count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && key_at(i + lane) == prefix));
-  int eq = before_me(count, 0, all);
+  int eq = 0, all;
+  if (sh.ties > need) {  // some of the equal keys go: which, by their order
+    int count = 0;
+    for (int i = i0; i < i1; i += 32)
+      count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && key_at(i + lane) == prefix));
+    eq = before_me(count, 0, all);
+  } else {
+    need = 0x7fffffff;
+  }
   int holes = 0, sources = 0;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
     const bool in = i + lane < i1;
     const uint32_t key = in ? key_at(i + lane) : 0u;
@@ -360,6 +382,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
   // ---- 3. the lists, then the rows
   int* hole_list = p.lists + (size_t)bh * 2 * p.n_keep;
   int* source_list = hole_list + p.n_keep;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
     const unsigned keep = keep_bits[i / 32], below = (1u << lane) - 1u;
     const int j = j0 + i + lane;
@@ -370,14 +393,29 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS) kv4_evict_kernel(const Kv4E
     if ((s >> lane) & 1u) source_list[sources + __popc(s & below)] = j;
     holes += __popc(h);
     sources += __popc(s);
-    if (in && stays && front) {
-      kept[j] = j;
-      if (w_out != w) w_out[j] = w[j];
-      if (pos_out != pos) pos_out[j] = pos[j];
+    if (in && stays && front) kept[j] = j;
+  }
+  __syncthreads();  // keep_bits of other warps
+  if (w_out != w || pos_out != pos) {
+    const int front = min(n, p.n_keep - j0);
+    for (int i = tid; i < front; i += 8 * KV4_EVICT_THREADS) {  // 8 slots a thread in flight
+      float a[8];
+      int c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = i + k * KV4_EVICT_THREADS;
+        a[k] = at < front ? w[j0 + at] : 0.f;
+        c[k] = at < front ? pos[j0 + at] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = i + k * KV4_EVICT_THREADS;
+        if (at < front && ((keep_bits[at / 32] >> lane) & 1u)) w_out[j0 + at] = a[k], pos_out[j0 + at] = c[k];
+      }
     }
   }
   cluster.sync();  // the lists are complete, and nobody reads weights or positions below n_keep any more
-  constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 4;  // 16 bytes of codes a lane
+  constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 2;  // 16 bytes of codes a lane
   const int sub = lane % LANES;
   for (int m0 = (rank * KV4_EVICT_WARPS + warp) * ROWS * DEEP; m0 < moves; m0 += CL * KV4_EVICT_WARPS * ROWS * DEEP) {
     uint4 kc[DEEP], vc[DEEP];
