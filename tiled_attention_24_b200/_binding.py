@@ -375,24 +375,43 @@ def attn_fwd_fp8(q, qs, k, ks, v, vs, o, lse, causal: bool, scale: float, rotate
     _check("attn_fwd_fp8", rc)
 
 
-def _on_device(*ts):
-    """The device all given tensors are on, as a context that makes it the current
-    one (a launch goes to the current device, whatever memory it points at)."""
-    dev = ts[0].device
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
-    return torch.cuda.device(dev)
+def _tensors(fn, *specs):
+    """(tensor or None, shape, dtype, name) tuples: every tensor must be contiguous, of
+    exactly that shape and dtype, and on the CUDA device of the first.  One pass
+    over plain integers: these calls are a decode step's, their checks count."""
+    dev = specs[0][0].get_device()
+    for t, shape, dtype, name in specs:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            raise ValueError(f"{fn}: tensors must be contiguous CUDA tensors on one device ({name}: {t.device})")
+    return dev
 
 
-def _expect_kv4(B, Hkv, cap, d, **arrays):
-    """Shapes and types of a 4-bit cache's arrays (those given as codes, scales,
-    fp32 or int32 per slot, int32 per sequence)."""
-    specs = {"c": ((B, Hkv, cap, d // 2), _U8), "s": ((B, Hkv, cap, d // 32), _BF16),
-             "w": ((B, Hkv, cap), _F32), "p": ((B, Hkv, cap), _I32), "b": ((B,), _I32)}
-    for name, (kind, t) in arrays.items():
-        if t is not None:
-            _expect((t, *specs[kind], name))
+def _call(fn, dev, stream, *args):
+    """The C call with the tensors' device current (a launch goes to the current
+    device, whatever memory it points at) and that device's current stream unless
+    one is given."""
+    here = torch.cuda.current_device()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    try:
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev)
+        elif isinstance(stream, torch.cuda.Stream):
+            stream = stream.cuda_stream
+        rc = getattr(_lib or load(), fn)(*args, int(stream))
+    finally:
+        if here != dev:
+            torch.cuda.set_device(here)
+    if rc != ATTN_OK:
+        raise AttnError(fn, rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _nbytes(t) -> int:
@@ -402,30 +421,25 @@ def _nbytes(t) -> int:
 def attn_kv4_append(k, v, kc, ks, vc, vs, starts, counts=None, weights=None, positions=None, next_pos=None, stream=None):
     """Quantise k, v [B,Hkv,n,d] bf16 and write them to slots starts[b] + i of a 4-bit
     cache (kc, vc uint8 [B,Hkv,capacity,d/2], ks, vs bf16 [B,Hkv,capacity,d/32])."""
-    _need_cuda(k, v, kc, ks, vc, vs, starts, counts, weights, positions, next_pos)
     B, Hkv, n, d = k.shape
     cap = kc.shape[2]
-    _expect((k, (B, Hkv, n, d), _BF16, "k"), (v, (B, Hkv, n, d), _BF16, "v"))
-    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), starts=("b", starts),
-                counts=("b", counts), weights=("w", weights), positions=("p", positions), next_pos=("b", next_pos))
-    with _on_device(k, v, kc, ks, vc, vs, starts, counts, weights, positions, next_pos):
-        rc = load().attn_kv4_append(_ptr(k), _ptr(v), _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(starts),
-                                    _ptr(counts), _ptr(weights), _ptr(positions), _ptr(next_pos), B, Hkv, n, cap, d,
-                                    _stream(stream))
-    _check("attn_kv4_append", rc)
+    codes, scales, slots = (B, Hkv, cap, d // 2), (B, Hkv, cap, d // 32), (B, Hkv, cap)
+    dev = _tensors("attn_kv4_append", (k, (B, Hkv, n, d), _BF16, "k"), (v, (B, Hkv, n, d), _BF16, "v"),
+                   (kc, codes, _U8, "kc"), (ks, scales, _BF16, "ks"), (vc, codes, _U8, "vc"), (vs, scales, _BF16, "vs"),
+                   (starts, (B,), _I32, "starts"), (counts, (B,), _I32, "counts"), (weights, slots, _F32, "weights"),
+                   (positions, slots, _I32, "positions"), (next_pos, (B,), _I32, "next_pos"))
+    _call("attn_kv4_append", dev, stream, k.data_ptr(), v.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+          vs.data_ptr(), starts.data_ptr(), _at(counts), _at(weights), _at(positions), _at(next_pos), B, Hkv, n, cap, d)
 
 
 def attn_kv4_read(codes, scales, out, starts=None, stream=None):
     """Values of slots starts[b] + i (from slot 0 without starts) as bf16 [B,Hkv,n,d]."""
-    _need_cuda(codes, scales, out, starts)
     B, Hkv, n, d = out.shape
     cap = codes.shape[2]
-    _expect((out, (B, Hkv, n, d), _BF16, "out"))
-    _expect_kv4(B, Hkv, cap, d, codes=("c", codes), scales=("s", scales), starts=("b", starts))
-    with _on_device(codes, scales, out, starts):
-        rc = load().attn_kv4_read(_ptr(codes), _ptr(scales), _ptr(out), _ptr(starts), B, Hkv, n, cap, d,
-                                  _stream(stream))
-    _check("attn_kv4_read", rc)
+    dev = _tensors("attn_kv4_read", (codes, (B, Hkv, cap, d // 2), _U8, "codes"),
+                   (scales, (B, Hkv, cap, d // 32), _BF16, "scales"), (out, (B, Hkv, n, d), _BF16, "out"),
+                   (starts, (B,), _I32, "starts"))
+    _call("attn_kv4_read", dev, stream, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), _at(starts), B, Hkv, n, cap, d)
 
 
 def attn_decode_kv4_splits(B: int, Hq: int, Hkv: int, capacity: int, d: int) -> int:
@@ -441,17 +455,16 @@ def attn_decode_kv4(q, kc, ks, vc, vs, o, lse, seqlens, scale: float, num_splits
                     stream=None):
     """Decode over a 4-bit cache: q, o [B,Hq,1,d] bf16, lse [B,Hq,1] fp32, live slots
     [0, seqlens[b]); weights [B,Hkv,capacity] fp32 grows by the attention weights."""
-    _need_cuda(q, kc, ks, vc, vs, o, lse, seqlens, workspace, weights)
     B, Hq, _, d = q.shape
     Hkv, cap = kc.shape[1], kc.shape[2]
-    _expect((q, (B, Hq, 1, d), _BF16, "q"), (o, (B, Hq, 1, d), _BF16, "o"), (lse, (B, Hq, 1), _F32, "lse"))
-    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), seqlens=("b", seqlens),
-                weights=("w", weights))
-    with _on_device(q, kc, ks, vc, vs, o, lse, seqlens, workspace, weights):
-        rc = load().attn_decode_kv4(_ptr(q), _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(o), _ptr(lse),
-                                    _ptr(weights), _ptr(seqlens), B, Hq, Hkv, cap, d, float(scale), int(num_splits),
-                                    _ptr(workspace), _nbytes(workspace), _stream(stream))
-    _check("attn_decode_kv4", rc)
+    codes, scales = (B, Hkv, cap, d // 2), (B, Hkv, cap, d // 32)
+    dev = _tensors("attn_decode_kv4", (q, (B, Hq, 1, d), _BF16, "q"), (kc, codes, _U8, "kc"), (ks, scales, _BF16, "ks"),
+                   (vc, codes, _U8, "vc"), (vs, scales, _BF16, "vs"), (o, (B, Hq, 1, d), _BF16, "o"),
+                   (lse, (B, Hq, 1), _F32, "lse"), (seqlens, (B,), _I32, "seqlens"),
+                   (weights, (B, Hkv, cap), _F32, "weights"), (workspace, workspace.shape, workspace.dtype, "workspace"))
+    _call("attn_decode_kv4", dev, stream, q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+          o.data_ptr(), lse.data_ptr(), _at(weights), seqlens.data_ptr(), B, Hq, Hkv, cap, d, float(scale),
+          int(num_splits), workspace.data_ptr(), _nbytes(workspace))
 
 
 def attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nkv: int, d: int) -> int:
@@ -463,22 +476,19 @@ def attn_key_weights(q, k, lse, weights, causal: bool, scale: float, workspace=N
     """Attention weight of each key of a prompt: q [B,Hq,Nq,d], k [B,Hkv,Nkv,d] bf16, lse
     [B,Hq,Nq] (the forward's) -> the first Nkv entries of the rows of weights
     [B,Hkv,>=Nkv] fp32."""
-    _need_cuda(q, k, lse, weights, workspace, seqlens)
     B, Hq, Nq, d = q.shape
     Hkv, Nkv = k.shape[1], k.shape[2]
     if weights.dim() != 3 or weights.shape[2] < Nkv:
         raise ValueError(f"weights: expected rows of at least {Nkv} entries, got {tuple(weights.shape)}")
     stride = weights.shape[2]
-    _expect((q, (B, Hq, Nq, d), _BF16, "q"), (k, (B, Hkv, Nkv, d), _BF16, "k"), (lse, (B, Hq, Nq), _F32, "lse"),
-            (weights, (B, Hkv, stride), _F32, "weights"))
-    if seqlens is not None:
-        _expect((seqlens, (B,), _I32, "seqlens"))
-    with _on_device(q, k, lse, weights, workspace, seqlens):
-        rc = load().attn_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(weights), _ptr(seqlens), B, Hq, Hkv, Nq, Nkv,
-                                     d, int(bool(causal)), int(bool(accumulate)), float(scale), stride,
-                                     _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-                                     _stream(stream))
-    _check("attn_key_weights", rc)
+    specs = [(q, (B, Hq, Nq, d), _BF16, "q"), (k, (B, Hkv, Nkv, d), _BF16, "k"), (lse, (B, Hq, Nq), _F32, "lse"),
+             (weights, (B, Hkv, stride), _F32, "weights"), (seqlens, (B,), _I32, "seqlens")]
+    if workspace is not None:
+        specs.append((workspace, workspace.shape, workspace.dtype, "workspace"))
+    dev = _tensors("attn_key_weights", *specs)
+    _call("attn_key_weights", dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), _at(seqlens),
+          B, Hq, Hkv, Nq, Nkv, d, int(bool(causal)), int(bool(accumulate)), float(scale), stride, _at(workspace),
+          0 if workspace is None else _nbytes(workspace))
 
 
 def attn_kv4_evict_workspace_bytes(B: int, Hkv: int, capacity: int, n_keep: int) -> int:
@@ -489,20 +499,19 @@ def attn_kv4_evict(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weight
                    n_recent: int, workspace, stream=None):
     """Keep n_keep = kept.shape[2] slots of every (batch, cache head): the n_recent newest,
     then those of the largest weight; kept int32 [B,Hkv,n_keep] gets their old slots."""
-    _need_cuda(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weights_out, positions_out, kept, workspace)
     B, Hkv, cap = kc.shape[:3]
     d = 2 * kc.shape[3]
     n_keep = kept.shape[2]
-    _expect((kept, (B, Hkv, n_keep), _I32, "kept"))
-    _expect_kv4(B, Hkv, cap, d, kc=("c", kc), ks=("s", ks), vc=("c", vc), vs=("s", vs), weights=("w", weights),
-                positions=("p", positions), seqlens=("b", seqlens), next_pos=("b", next_pos),
-                weights_out=("w", weights_out), positions_out=("p", positions_out))
-    with _on_device(kc, ks, vc, vs, weights, positions, seqlens, next_pos, weights_out, positions_out, kept, workspace):
-        rc = load().attn_kv4_evict(_ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), _ptr(weights), _ptr(positions),
-                                   _ptr(seqlens), _ptr(next_pos), _ptr(weights_out), _ptr(positions_out), _ptr(kept),
-                                   B, Hkv, cap, d, n_keep, int(n_recent), _ptr(workspace), _nbytes(workspace),
-                                   _stream(stream))
-    _check("attn_kv4_evict", rc)
+    codes, scales, slots = (B, Hkv, cap, d // 2), (B, Hkv, cap, d // 32), (B, Hkv, cap)
+    dev = _tensors("attn_kv4_evict", (kc, codes, _U8, "kc"), (ks, scales, _BF16, "ks"), (vc, codes, _U8, "vc"),
+                   (vs, scales, _BF16, "vs"), (weights, slots, _F32, "weights"), (positions, slots, _I32, "positions"),
+                   (seqlens, (B,), _I32, "seqlens"), (next_pos, (B,), _I32, "next_pos"),
+                   (weights_out, slots, _F32, "weights_out"), (positions_out, slots, _I32, "positions_out"),
+                   (kept, (B, Hkv, n_keep), _I32, "kept"), (workspace, workspace.shape, workspace.dtype, "workspace"))
+    _call("attn_kv4_evict", dev, stream, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), weights.data_ptr(),
+          positions.data_ptr(), seqlens.data_ptr(), next_pos.data_ptr(), weights_out.data_ptr(),
+          positions_out.data_ptr(), kept.data_ptr(), B, Hkv, cap, d, n_keep, int(n_recent), workspace.data_ptr(),
+          _nbytes(workspace))
 
 
 def attn_check_status(stream=None) -> int:
