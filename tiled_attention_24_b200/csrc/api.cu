@@ -414,6 +414,41 @@ static int launch_key_weights(const void* q, const void* k, int B, int Hq, int H
   return ATTN_OK;
 }
 
+// A launch that may be set up while the grid before it in the stream still runs; it
+// waits for that grid's end itself (griddepcontrol.wait).
+template <typename K, typename... Args>
+static int launch_after(K kernel, unsigned grid, unsigned threads, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int NG>
+static int launch_decode_kv4(const ta::DecKv4Params& p, attn_bf16_t* o, float* lse, float* weights, cudaStream_t st) {
+  constexpr int D = 32 * NG, W = ta::KV4_FINISH_THREADS / 32;
+  const int rc = set_smem_attr(ta::decode_kv4_kernel<NG>, ta::DecKv4Cfg<NG>::SMEM);
+  if (rc != ATTN_OK) return rc;
+  const unsigned grid = (unsigned)((p.pieces + ta::KV4_WARPS - 1) / ta::KV4_WARPS);
+  ta::decode_kv4_kernel<NG><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<NG>::SMEM, st>>>(p);
+  if (cudaPeekAtLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  const long long rows = (long long)p.B * p.Hkv * p.group, heads = (long long)p.B * p.Hkv;
+  const bool wide = p.pieces >= 8 * heads * p.blocks;
+  const long long merge = wide ? rows * NG : (rows + W - 1) / W;
+  const long long more = weights ? heads * ((p.cap + ta::KV4_FINISH_SLOTS - 1) / ta::KV4_FINISH_SLOTS) : 0;
+  if (merge + more > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return wide ? launch_after(ta::decode_kv4_finish_kernel<D, true>, (unsigned)(merge + more), ta::KV4_FINISH_THREADS, st,
+                             p, o, lse, weights, (int)merge)
+              : launch_after(ta::decode_kv4_finish_kernel<D, false>, (unsigned)(merge + more), ta::KV4_FINISH_THREADS,
+                             st, p, o, lse, weights, (int)merge);
+}
+
 // One cluster per (batch, cache head), of 1 to 8 CTAs: as many as fill the 296 that
 // run at once (two on an SM) with slices of at least 2048 slots, and no fewer
 // than keep a slice's keys in shared memory.
@@ -1051,10 +1086,9 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   if (rc != ATTN_OK) return rc;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (B == 0 || Hq == 0) return ATTN_OK;
-  if (weights && (long long)B * Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
   if (!q || !kc || !ks || !vc || !vs || !o || !lse || !seqlens || !workspace) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kc) || !aligned16(ks) || !aligned16(vc) || !aligned16(vs) || !aligned16(o) ||
-      !aligned4(lse) || !aligned4(weights) || !aligned4(seqlens) || !aligned16(workspace))
+      !aligned4(lse) || !aligned16(weights) || !aligned4(seqlens) || !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
   const Kv4DecodeWs ws = kv4_decode_ws(B, Hq, Hkv, capacity, d, num_splits, weights != nullptr);
   if (workspace_bytes < ws.bytes) return ATTN_ERR_INVALID_ARG;
@@ -1078,29 +1112,18 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   p.sl2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((p.pieces + ta::KV4_WARPS - 1) / ta::KV4_WARPS), rows = (unsigned)(B * Hq);
-  if (d == 128) {
-    if ((rc = set_smem_attr(ta::decode_kv4_kernel<4>, ta::DecKv4Cfg<4>::SMEM)) != ATTN_OK) return rc;
-    ta::decode_kv4_kernel<4><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<4>::SMEM, st>>>(p);
-    ta::decode_kv4_merge_kernel<128><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
-  } else {
-    if ((rc = set_smem_attr(ta::decode_kv4_kernel<2>, ta::DecKv4Cfg<2>::SMEM)) != ATTN_OK) return rc;
-    ta::decode_kv4_kernel<2><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<2>::SMEM, st>>>(p);
-    ta::decode_kv4_merge_kernel<64><<<rows, ta::KV4_MERGE_THREADS, 0, st>>>(p, o, lse);
-  }
-  if (weights)
-    ta::decode_kv4_weights_kernel<<<dim3((unsigned)((capacity + 255) / 256), (unsigned)(B * Hkv)), 256, 0, st>>>(
-        p.x, lse, weights, seqlens, Hq, Hkv, capacity);
+  rc = d == 128 ? launch_decode_kv4<4>(p, o, lse, weights, st) : launch_decode_kv4<2>(p, o, lse, weights, st);
+  if (rc != ATTN_OK) return rc;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 // Parts the query tiles of a pair of key tiles are cut into: about 8 items for
 // each of 148 SMs, so that the uneven items of a causal prompt even out, but at
-// least 8 query tiles a part (an item's start and end cost about one).
+// least 4 query tiles a part (an item's start and end cost about one).
 static int key_weights_parts(int B, int Hq, int Hkv, int Nq, int Nkv) {
   const long long pairs = (long long)B * Hkv * ((Nkv + 255) / 256), q_tiles = ((long long)(Hq / Hkv) * Nq + 127) / 128;
   const long long want = (8LL * 148 + pairs - 1) / pairs;
-  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 64), q_tiles / 8));
+  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, 64), q_tiles / 4));
 }
 
 static int key_weights_shape(int B, int Hq, int Hkv, int Nq, int Nkv, int d) {
@@ -1162,7 +1185,9 @@ int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* ls
   rc = d == 128 ? launch_key_weights<128>(q, k, B, Hq, Hkv, Nq, Nkv, p, st)
                 : launch_key_weights<64>(q, k, B, Hq, Hkv, Nq, Nkv, p, st);
   if (rc != ATTN_OK) return rc;
-  if (p.parts > 1) ta::key_weights_join_kernel<<<columns, 256, 0, st>>>(p);
+  if (p.parts > 1 &&
+      (rc = launch_after(ta::key_weights_join_kernel, columns.x * columns.y, 256, st, p, (int)columns.x)) != ATTN_OK)
+    return rc;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -12,8 +12,9 @@
 // A piece may begin and end inside a row; each (row, piece) leaves a partial
 // output, its sum and the exponent both are relative to, and a second kernel
 // merges a row's partials.  A weight needs the log-sum-exp of the whole row, so
-// the first kernel leaves the scores x in the workspace and a last kernel turns
-// them into weights.
+// the first kernel leaves the scores x in the workspace, fp32 (8 bytes a slot and
+// head written and read, mostly in L2, against 4.5 bits a channel to read K
+// again), and the second one turns them into weights.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -142,7 +143,8 @@ __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w;
 //     tile through a second product with the constant -8: summed up over a long
 //     row it would swamp the result.
 template <int NG>
-__global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS) decode_kv4_kernel(const DecKv4Params p) {
+__global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS)
+    decode_kv4_kernel(const __grid_constant__ DecKv4Params p) {
   using C = DecKv4Cfg<NG>;
   using T = typename Kv4Piece<NG>::T;
   constexpr int D = C::D;
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     fence_proxy_async_smem();
   }
   __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the finish may line up behind this grid
 
   // ---- this warp's piece: tiles [first, first + mine) of the batch
   const int per_entry = p.Hkv * p.blocks;  // items of a batch entry
@@ -474,80 +477,151 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   }
 }
 
-// Merge of a row's partials, one CTA per (batch, query head): with f = 2^(M_c - max M),
-// O = sum f O_c / sum f l_c, LSE = ln 2 (max M + log2 sum f l_c).  A row without
-// slots has no partial; a NaN in a live slot stays one.
-constexpr int KV4_MERGE_THREADS = 256;
-template <int D>
-__global__ void __launch_bounds__(KV4_MERGE_THREADS)
-    decode_kv4_merge_kernel(const DecKv4Params p, uint16_t* __restrict__ o, float* __restrict__ lse) {
-  constexpr int LANES = D / 4, GROUPS = KV4_MERGE_THREADS / LANES;  // float4 of channels; partials side by side
-  __shared__ float s_max[KV4_MERGE_THREADS / 32];
-  __shared__ float4 s_o[GROUPS][LANES];
-  __shared__ float s_l[GROUPS];
-  const int Hq = p.Hkv * p.group, b = blockIdx.x / Hq, h = blockIdx.x % Hq;
-  const int tiles = kv4_tiles(p.seqlens, b, p.cap);
-  const int lane4 = threadIdx.x % LANES, grp = threadIdx.x / LANES;
-  uint16_t* orow = o + (size_t)blockIdx.x * D;
-  if (tiles == 0) {
-    if (threadIdx.x < LANES) *reinterpret_cast<uint2*>(orow + 4 * lane4) = make_uint2(0, 0);
-    if (threadIdx.x == 0) lse[blockIdx.x] = -INFINITY;
-    return;
-  }
-  const int per_entry = p.Hkv * p.blocks;
-  const int total = kv4_tiles_before(p.seqlens, p.B, p.cap) * per_entry;
-  const int per = kv4_per_piece(total, p.pieces);
+// A row's partials: the first one's index and how many (none without slots); whole warp
+struct Kv4Parts {
+  size_t first;
+  int n;
+};
+__device__ __forceinline__ Kv4Parts kv4_row_parts(const DecKv4Params& p, int row) {
+  const int Hq = p.Hkv * p.group, b = row / Hq, h = row - b * Hq;
+  const int tiles = kv4_tiles(p.seqlens, b, p.cap), per_entry = p.Hkv * p.blocks;
+  const int per = kv4_per_piece(kv4_tiles_before(p.seqlens, p.B, p.cap) * per_entry, p.pieces);
   const int in_entry = h / p.group * p.blocks + h % p.group / 8, head = h % p.group % 8;
-  const int item = b * per_entry + in_entry;
-  const int t0 = kv4_tiles_before(p.seqlens, b, p.cap) * per_entry + in_entry * tiles;
-  const int c0 = t0 / per, n = (t0 + tiles - 1) / per - c0 + 1;  // pieces the row lies in
-  const size_t part = (size_t)(c0 + item) * p.per_block + head;
-  const float2* ml = p.ml_part + part;
+  const int t0 = kv4_tiles_before(p.seqlens, b, p.cap) * per_entry + in_entry * tiles, c0 = t0 / per;
+  Kv4Parts r;
+  r.first = (size_t)(c0 + b * per_entry + in_entry) * p.per_block + head;
+  r.n = tiles == 0 ? 0 : (t0 + tiles - 1) / per - c0 + 1;
+  return r;
+}
+// max of the partials' exponents and log2 sum_c 2^(M_c - max) l_c; whole warp
+__device__ __forceinline__ float kv4_parts_max(const float2* ml, int step, int n) {
   float mx = -INFINITY;
-  for (int c = threadIdx.x; c < n; c += KV4_MERGE_THREADS) mx = fmaxf(mx, ml[(size_t)c * p.per_block].x);
+  for (int c = threadIdx.x & 31; c < n; c += 32) mx = fmaxf(mx, ml[(size_t)c * step].x);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
-  __syncthreads();
+  return mx;
+}
+__device__ __forceinline__ float kv4_part_factor(float M, float mx) { return M == mx ? 1.f : ex2(M - mx); }  // all NaN: no max
+__device__ __forceinline__ float kv4_lse2(float mx, float l) { return (mx == -INFINITY ? 0.f : mx) + log2f(l); }
+
+// What the pieces left becomes the outputs, in one launch.  The first CTAs merge: with
+// f = 2^(M_c - max M), O = sum f O_c / sum f l_c, LSE = ln 2 (max M + log2 sum f l_c);
+// a row without slots has no partial, a NaN in a live slot stays one.  WIDE (8
+// partials a row or more): a CTA per row and 32 channels, 32 partials at a time;
+// else a warp per row.  The other CTAs, where weights are wanted, take 1024
+// slots of a cache head each: w_j += sum_h 2^(x_hj - lse_h log2 e), with the rows'
+// log-sum-exps worked out again from the partials' (M, l), a few KB.
+constexpr int KV4_FINISH_THREADS = 256, KV4_FINISH_SLOTS = 4 * KV4_FINISH_THREADS, KV4_FINISH_HEADS = 64;
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(KV4_FINISH_THREADS)
+    decode_kv4_finish_kernel(const __grid_constant__ DecKv4Params p, uint16_t* __restrict__ o, float* __restrict__ lse,
+                             float* __restrict__ weights, int merge_blocks) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if ((int)blockIdx.x >= merge_blocks) {
+    // ---- weights
+    __shared__ float s_lse2[KV4_FINISH_HEADS];
+    const int per = (p.cap + KV4_FINISH_SLOTS - 1) / KV4_FINISH_SLOTS, at = blockIdx.x - merge_blocks;
+    const int bhk = at / per, j = (at - bhk * per) * KV4_FINISH_SLOTS + 4 * tid;
+    const int len = min(max(p.seqlens[bhk / p.Hkv], 0), p.cap);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (j - 4 * tid >= len) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int h0 = 0; h0 < p.group; h0 += KV4_FINISH_HEADS) {
+      const int heads = min(KV4_FINISH_HEADS, p.group - h0);
+      __syncthreads();
+      for (int h = warp; h < heads; h += KV4_FINISH_THREADS / 32) {
+        const Kv4Parts parts = kv4_row_parts(p, bhk * p.group + h0 + h);
+        const float2* ml = p.ml_part + parts.first;
+        const float mx = kv4_parts_max(ml, p.per_block, parts.n);
+        float l = 0.f;
+        for (int c = lane; c < parts.n; c += 32) {
+          const float2 v = ml[(size_t)c * p.per_block];
+          l = fmaf(kv4_part_factor(v.x, mx), v.y, l);
+        }
 #pragma unroll
-  for (int k = 0; k < KV4_MERGE_THREADS / 32; ++k) mx = fmaxf(mx, s_max[k]);
+        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        if (lane == 0) s_lse2[h] = kv4_lse2(mx, l);
+      }
+      __syncthreads();
+      if (j < len) {
+        const float* x = p.x + ((size_t)bhk * p.group + h0) * p.cap + j;
+#pragma unroll 4
+        for (int h = 0; h < heads; ++h) {
+          const float4 v = *reinterpret_cast<const float4*>(x + (size_t)h * p.cap);
+          const float l2 = s_lse2[h];
+          sum.x += ex2(v.x - l2), sum.y += ex2(v.y - l2), sum.z += ex2(v.z - l2), sum.w += ex2(v.w - l2);
+        }
+      }
+    }
+    float* w = weights + (size_t)bhk * p.cap + j;
+    if (j + 4 <= len) {
+      float4 v = *reinterpret_cast<float4*>(w);
+      v.x += sum.x, v.y += sum.y, v.z += sum.z, v.w += sum.w;
+      *reinterpret_cast<float4*>(w) = v;
+    } else if (j < len) {
+      w[0] += sum.x;
+      if (j + 1 < len) w[1] += sum.y;
+      if (j + 2 < len) w[2] += sum.z;
+    }
+    return;
+  }
+  // ---- merge
+  constexpr int LANES = WIDE ? 8 : D / 4;  // float4 of channels
+  constexpr int GROUPS = (WIDE ? KV4_FINISH_THREADS : 32) / LANES;
+  const int row = WIDE ? blockIdx.x / (D / 32) : blockIdx.x * (KV4_FINISH_THREADS / 32) + warp;
+  const int first = WIDE ? blockIdx.x % (D / 32) * 8 : 0;
+  if (row >= p.B * p.Hkv * p.group) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the one it follows
+    return;
+  }
+  const int lane4 = (WIDE ? tid : lane) % LANES, grp = (WIDE ? tid : lane) / LANES;
+  uint2* out = reinterpret_cast<uint2*>(o + (size_t)row * D) + first + lane4;
+  const Kv4Parts parts = kv4_row_parts(p, row);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (parts.n == 0) {
+    if (grp == 0) *out = make_uint2(0, 0);
+    if (grp == 0 && first + lane4 == 0) lse[row] = -INFINITY;
+    return;
+  }
+  const float2* ml = p.ml_part + parts.first;
+  const float mx = kv4_parts_max(ml, p.per_block, parts.n);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
 #pragma unroll 4
-  for (int c = grp; c < n; c += GROUPS) {
+  for (int c = grp; c < parts.n; c += GROUPS) {
     const float2 v = ml[(size_t)c * p.per_block];
-    const float4 w = reinterpret_cast<const float4*>(p.o_part + (part + (size_t)c * p.per_block) * D)[lane4];
-    const float f = v.x == mx ? 1.f : ex2(v.x - mx);  // all NaN: no max, but NaN sums
+    const float4 w = reinterpret_cast<const float4*>(p.o_part + (parts.first + (size_t)c * p.per_block) * D)[first + lane4];
+    const float f = kv4_part_factor(v.x, mx);
     l = fmaf(f, v.y, l);
     a.x = fmaf(f, w.x, a.x), a.y = fmaf(f, w.y, a.y), a.z = fmaf(f, w.z, a.z), a.w = fmaf(f, w.w, a.w);
   }
-  s_o[grp][lane4] = a;
-  if (lane4 == 0) s_l[grp] = l;
-  __syncthreads();
-  if (threadIdx.x >= LANES) return;
-  for (int k = 1; k < GROUPS; ++k) {
-    const float4 w = s_o[k][lane4];
-    a.x += w.x, a.y += w.y, a.z += w.z, a.w += w.w;
-    l += s_l[k];
+#pragma unroll
+  for (int k = LANES; k < 32; k <<= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, k), a.y += __shfl_xor_sync(0xffffffffu, a.y, k);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, k), a.w += __shfl_xor_sync(0xffffffffu, a.w, k);
+    l += __shfl_xor_sync(0xffffffffu, l, k);
+  }
+  if (WIDE) {
+    __shared__ float4 s_o[KV4_FINISH_THREADS / 32][8];
+    __shared__ float s_l[KV4_FINISH_THREADS / 32];
+    if (lane < 8) s_o[warp][lane] = a;
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (tid >= 8) return;
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < KV4_FINISH_THREADS / 32; ++k) {
+      const float4 w = s_o[k][tid];
+      a.x += w.x, a.y += w.y, a.z += w.z, a.w += w.w;
+      l += s_l[k];
+    }
+  } else if (grp != 0) {
+    return;
   }
   const float inv = 1.f / l;
-  *reinterpret_cast<uint2*>(orow + 4 * lane4) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-  if (threadIdx.x == 0) lse[blockIdx.x] = ((mx == -INFINITY ? 0.f : mx) + log2f(l)) * 0.69314718055994531f;
-}
-
-// w_j += sum_h 2^(x_hj - lse_h log2 e) over the query heads of one cache head
-__global__ void __launch_bounds__(256)
-    decode_kv4_weights_kernel(const float* __restrict__ x, const float* __restrict__ lse, float* __restrict__ weights,
-                              const int* __restrict__ seqlens, int Hq, int Hkv, int cap) {
-  const int bhk = blockIdx.y, group = Hq / Hkv;
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= min(max(seqlens[bhk / Hkv], 0), cap)) return;
-  float sum = 0.f;
-  for (int h = 0; h < group; ++h) {
-    const size_t bh = (size_t)bhk * group + h;
-    sum += ex2(x[bh * cap + j] - lse[bh] * 1.4426950408889634f);
-  }
-  weights[(size_t)bhk * cap + j] += sum;
+  *out = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+  if (first + lane4 == 0) lse[row] = kv4_lse2(mx, l) * 0.69314718055994531f;
 }
 
 }  // namespace ta

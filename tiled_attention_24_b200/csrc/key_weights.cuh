@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = bars->tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may line up behind this grid
 
   if (warp == 8) {
     // ================================================================ producer
@@ -436,10 +437,12 @@ __global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
 }
 
 // joins the parts, always in the same order
-__global__ void __launch_bounds__(256) key_weights_join_kernel(const KeyWeightsParams p) {
-  const int bhk = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) key_weights_join_kernel(const KeyWeightsParams p, int columns) {
+  const int bhk = blockIdx.x / columns, j = blockIdx.x % columns * 256 + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (j >= p.Nkv) return;
   float w = 0.f;
+#pragma unroll 8
   for (int k = 0; k < p.parts; ++k) w += p.parts_out[((size_t)k * p.BHkv + bhk) * p.Nkv + j];
   float* out = p.w + bhk * p.stride + j;
   *out = p.accumulate ? *out + w : w;

@@ -63,50 +63,45 @@ struct Kv4AppendParams {
   unsigned rows;              // B * Hkv * n
 };
 
-// One row by the 8 lanes of its pieces (lane u: channels 4u..4u+3 of each
-// group).  amax is taken on the bf16 bit patterns (ordered like the values,
-// infinities and NaNs on top).
+// One K and one V row by the 8 lanes of their pieces (lane u: channels 4u..4u+3 of
+// each of the 2 NG groups).  What a group needs once is done once: amax by a
+// butterfly that halves the groups a lane holds at each step, on pairs of bf16 bit
+// patterns (ordered like the values, infinities and NaNs on top); the scale and its
+// reciprocal by one lane (two where d = 64), which hands the reciprocal round.
 //
 // The codes need rne(x / s) exactly, without a divide per element: with
 // r = rn(1/s), fma(x, r, 6144) - 6144 is x r rounded to a multiple of 2^-11.
 // x and s have 8 significant bits, so a quotient of magnitude <= 7.6 is either
 // exactly k + 1/2 or at least 2^-2 / 255 > 9e-4 away from it, and x r is within
 // 5e-7 of the quotient: rounded to 2^-11 (at most 2.5e-4 away) the ties are
-// ties again and nothing else is one.  Adding 1.5 * 2^23 then rounds to even
-// and leaves the code in the low nibble.  |x / s| <= 7 (1 + 2^-8), so no code
-// exceeds 7.  Scales below 2^-100, where 1/s may overflow or s has lost bits,
-// take the divide and the clamp.
-template <int NG>
-__device__ __forceinline__ void kv4_quantize_row(const uint2 (&w)[NG], uint32_t (&half)[NG], uint32_t (&sc)[NG]) {
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const uint32_t a = w[g].x & 0x7FFF7FFFu, b = w[g].y & 0x7FFF7FFFu;
-    const uint32_t m2 = __vmaxu2(a, b);
-    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t bits = pack_bf16(__fdiv_rn(__uint_as_float(m << 16), 7.f), 0.f) & 0xFFFFu;
-    const float s = __uint_as_float(bits << 16);
-    const float x[4] = {__uint_as_float(w[g].x << 16), __uint_as_float(w[g].x & 0xFFFF0000u),
-                        __uint_as_float(w[g].y << 16), __uint_as_float(w[g].y & 0xFFFF0000u)};
-    uint32_t h = 0;
-    sc[g] = bits;
-    if (m >= 0x7F80u) {
-      sc[g] = 0x7FC0u;
-    } else if (s >= 0x1p-100f) {
-      const float r = __frcp_rn(s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float y = (fmaf(x[i], r, 6144.f) - 6144.f) + 12582912.f;
-        h |= (__float_as_uint(y) & 15u) << (4 * i);
-      }
-    } else if (s > 0.f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h |= ((uint32_t)max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s)))) & 15u) << (4 * i);
-    }
-    half[g] = h;
-  }
+// ties again and nothing else is one.  Adding and taking off 1.5 * 2^23 then rounds
+// to even.  |x / s| <= 7 (1 + 2^-8), so no code exceeds 7.  Four codes become a
+// halfword as the number sum 16^i (c_i + 8), whose digits are the nibbles with
+// their sign bits flipped.  Groups with an infinity or a NaN, and scales below
+// 2^-100, where 1/s may overflow or s has lost bits, are redone with the divide.
+//
+// Bound by HBM with this (4 x 16 heads x 4096 tokens, d = 128, 173 MB); a divide per
+// group and lane and integer packing took 14 instructions a value and 53 us.
+__device__ __forceinline__ uint32_t kv4_halfword(uint32_t lo, uint32_t hi, float r) {
+  const uint64_t rr = f2(r, r), six = f2(6144.f, 6144.f), nsix = f2(-6144.f, -6144.f);
+  const uint64_t big = f2(12582912.f, 12582912.f), nbig = f2(-12582912.f, -12582912.f);
+  uint64_t a = ffma2(f2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u)), rr, six);
+  uint64_t b = ffma2(f2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), rr, six);
+  a = fadd2(fadd2(fadd2(a, nsix), big), nbig);  // c0, c1
+  b = fadd2(fadd2(fadd2(b, nsix), big), nbig);  // c2, c3
+  float c0, c1;
+  f2_split(ffma2(b, f2(256.f, 256.f), a), c0, c1);                // c0 + 256 c2, c1 + 256 c3
+  const float n = fmaf(c1, 16.f, c0) + (8388608.f + 34952.f);     // + 0x8888, in the low bits
+  return (__float_as_uint(n) & 0xFFFFu) ^ 0x8888u;
+}
+__device__ __noinline__ uint32_t kv4_halfword_slow(uint32_t lo, uint32_t hi, uint32_t scale_bits) {
+  const float s = kv4_scale(scale_bits);
+  const float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
+                      __uint_as_float(hi & 0xFFFF0000u)};
+  uint32_t h = 0;
+  if (s > 0.f)  // neither zero nor NaN
+    for (int i = 0; i < 4; ++i) h |= ((uint32_t)max(-7, min(7, __float2int_rn(__fdiv_rn(x[i], s)))) & 15u) << (4 * i);
+  return h;
 }
 
 template <int NG>
@@ -119,25 +114,80 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
   const unsigned bh = (in ? row : 0u) / (unsigned)p.n;
   const int i = (int)((in ? row : 0u) - bh * (unsigned)p.n);
   const int b = (int)(bh / (unsigned)p.Hkv);
+  uint2 w[2 * NG];  // K groups, V groups; loaded before the slot is known to be live
+#pragma unroll
+  for (int g = 0; g < 2 * NG; ++g) {
+    const uint16_t* x = (g < NG ? p.k : p.v) + (size_t)row * D + 32 * (g % NG) + 4 * u;
+    w[g] = in ? *reinterpret_cast<const uint2*>(x) : make_uint2(0, 0);
+  }
   const int count = p.counts ? p.counts[b] : p.n;
   const long long slot = (long long)p.starts[b] + i;
   const bool live = in && i < count && slot >= 0 && slot < p.cap;
-  uint2 wk[NG], wv[NG];
+
+  uint32_t m[NG];  // amax of groups 2i (low half) and 2i + 1
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const size_t at = (size_t)row * D + 32 * g + 4 * u;
-    wk[g] = live ? *reinterpret_cast<const uint2*>(p.k + at) : make_uint2(0, 0);
-    wv[g] = live ? *reinterpret_cast<const uint2*>(p.v + at) : make_uint2(0, 0);
+  for (int g = 0; g < 2 * NG; g += 2) {
+    uint32_t a[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t v = __vmaxu2(w[g + e].x & 0x7FFF7FFFu, w[g + e].y & 0x7FFF7FFFu);
+      a[e] = max(v & 0xFFFFu, v >> 16);
+    }
+    m[g / 2] = a[0] | (a[1] << 16);
   }
-  uint32_t hk[NG], hv[NG], sk[NG], sv[NG];
-  kv4_quantize_row<NG>(wk, hk, sk);
-  kv4_quantize_row<NG>(wv, hv, sv);
+  // halve the pairs held at each step; then lane u has pair `pair`, groups 2 pair, 2 pair + 1
+  int pair = 0, bit = 4;
+  if (NG == 4) {
+    const bool up = u & 4;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t give = up ? m[e] : m[(e + 2) % NG], keep = up ? m[(e + 2) % NG] : m[e];
+      m[e] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+    }
+    pair = up ? 2 : 0;
+    bit = 2;
+  }
+  {
+    const bool up = u & bit;
+    const uint32_t give = up ? m[0] : m[1], keep = up ? m[1] : m[0];
+    m[0] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    pair += up ? 1 : 0;
+  }
+#pragma unroll
+  for (int o = NG == 4 ? 1 : 2; o > 0; o >>= 1) m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+  const int mine = 2 * pair + (u & 1);  // this lane's group
+  const uint32_t top = (u & 1) ? m[0] >> 16 : m[0] & 0xFFFFu;
+  uint32_t bits = pack_bf16(__fdiv_rn(__uint_as_float(top << 16), 7.f), 0.f) & 0xFFFFu;
+  if (top >= 0x7F80u) bits = 0x7FC0u;
+  const float s = kv4_scale(bits);
+  const bool odd = !(s == 0.f || s >= 0x1p-100f);
+  const float r = s == 0.f ? 0.f : __frcp_rn(s);
+
+  uint32_t h[2 * NG];
+  const int base = (threadIdx.x & 24);
+#pragma unroll
+  for (int g = 0; g < 2 * NG; ++g) {
+    // the lane of the row that holds group g
+    const int from = NG == 4 ? ((g & 4) ? 4 : 0) | ((g & 2) ? 2 : 0) | (g & 1) : ((g & 2) ? 4 : 0) | (g & 1);
+    h[g] = kv4_halfword(w[g].x, w[g].y, __shfl_sync(0xffffffffu, r, base + from));
+  }
+  if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+    for (int g = 0; g < 2 * NG; ++g) {
+      const int from = NG == 4 ? ((g & 4) ? 4 : 0) | ((g & 2) ? 2 : 0) | (g & 1) : ((g & 2) ? 4 : 0) | (g & 1);
+      const uint32_t sb = __shfl_sync(0xffffffffu, bits, base + from);
+      if (__shfl_sync(0xffffffffu, (int)odd, base + from)) h[g] = kv4_halfword_slow(w[g].x, w[g].y, sb);
+    }
+  }
   if (!live) return;
   const size_t dst = (size_t)bh * p.cap + slot;
+  uint32_t hk[NG], hv[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) hk[g] = h[g], hv[g] = h[NG + g];
   reinterpret_cast<T*>(p.kc + dst * (D / 2))[u] = kv4_join(hk);
   reinterpret_cast<T*>(p.vc + dst * (D / 2))[u] = kv4_join(hv);
-  if (u == 0) *reinterpret_cast<T*>(p.ks + dst * NG) = kv4_join(sk);
-  if (u == 1) *reinterpret_cast<T*>(p.vs + dst * NG) = kv4_join(sv);
+  // every group's scale by the lane that made it (d = 64: by the first of the two)
+  if (NG == 4 || !(u & 2)) (mine < NG ? p.ks : p.vs)[dst * NG + mine % NG] = (uint16_t)bits;
   if (u == 2 && p.weights) p.weights[dst] = 0.f;
   if (u == 3 && p.positions) p.positions[dst] = p.next_pos[b] + i;
 }
