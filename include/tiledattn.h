@@ -437,7 +437,7 @@ ATTN_API int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn
  * weight grows by the sum of the softmax probabilities of its cache head's
  * query heads.  A sequence without live slots gets O = 0, LSE = -inf.
  *   q, o bf16 [B][Hq][1][d]; lse fp32 [B][Hq]; seqlens int32 [B] DEVICE;
- *   weights fp32 [B][Hkv][capacity] or NULL; num_splits, 1 to 1024: the live
+ *   weights fp32 [B][Hkv][capacity], 16-byte aligned, or NULL; num_splits, 1 to 1024: the live
  *   slots of the whole batch are cut into at most num_splits * B * Hkv equal
  *   pieces (times ceil(Hq / Hkv / 8)), whatever the sequences' lengths, never
  *   more than the GPU works on at once (attn_decode_kv4_splits: enough to fill

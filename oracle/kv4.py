@@ -67,14 +67,16 @@ def values(packed, scales):
 
 
 def decode(q, kc, ks, vc, vs, seqlens, scale):
-    """o [B,Hq,1,d], lse [B,Hq,1] and the probability mass per slot [B,Hkv,cap], with the
-    sums sum_j p |v| and max_j sum |q k| scale that error bounds are made of."""
+    """o [B,Hq,1,d], lse [B,Hq,1] and the probability mass per slot [B,Hkv,cap], with what
+    error bounds are made of: sum_j p |v| and sum_j p s (s: the scale of v's group), both
+    [B,Hq,1,d], and max_j sum |q k| scale."""
     q = _f64(q)
     B, Hq, _, d = q.shape
     Hkv, cap = kc.shape[1:3]
     G = Hq // Hkv
     o, lse = np.zeros((B, Hq, 1, d)), np.full((B, Hq, 1), -np.inf)
-    w, pv, sm = np.zeros((B, Hkv, cap)), np.zeros((B, Hq, 1, d)), np.zeros((B, Hq, 1))
+    w, sm = np.zeros((B, Hkv, cap)), np.zeros((B, Hq, 1))
+    pv, ps = np.zeros((B, Hq, 1, d)), np.zeros((B, Hq, 1, d))
     for b in range(B):
         n = min(max(int(seqlens[b]), 0), cap)
         if n == 0:
@@ -89,8 +91,9 @@ def decode(q, kc, ks, vc, vs, seqlens, scale):
                 o[b, a, 0], lse[b, a, 0] = p @ v, m + np.log(e.sum())
                 w[b, h, :n] += p
                 pv[b, a, 0] = p @ np.abs(v)
+                ps[b, a, 0] = p @ np.repeat(_f64(vs[b, h, :n]), GROUP, axis=-1)
                 sm[b, a, 0] = (np.abs(k) @ np.abs(q[b, a, 0])).max() * scale
-    return o, lse, w, pv, sm
+    return o, lse, w, pv, ps, sm
 
 
 def key_weights(q, k, lse, causal, scale, seqlens=None):

@@ -98,7 +98,7 @@ def test_oracle_decode_matches_softmax():
     kc, ks = O.quantize(torch.randn(B, Hkv, cap, d, generator=g).bfloat16())
     vc, vs = O.quantize(torch.randn(B, Hkv, cap, d, generator=g).bfloat16())
     lens = [32, 9]
-    o, lse, w, _, _ = O.decode(q, O.pack(kc), ks, O.pack(vc), vs, lens, 0.125)
+    o, lse, w = O.decode(q, O.pack(kc), ks, O.pack(vc), vs, lens, 0.125)[:3]
     for b, n in enumerate(lens):
         k = torch.from_numpy(kc[b, :, :n] * np.repeat(ks[b, :, :n], 32, axis=-1)).double().repeat_interleave(2, dim=0)
         v = torch.from_numpy(vc[b, :, :n] * np.repeat(vs[b, :, :n], 32, axis=-1)).double().repeat_interleave(2, dim=0)
@@ -152,6 +152,8 @@ def test_decode_validation(lib):
     assert call(S=1025) == -1 and call(scale=0.0) == -1 and call(scale=float("inf")) == -1 and call(nb=n - 1) == -1
     assert call(lens=None) == -1 and call(ws=None) == -1 and call(q=ODD) == -3 and call(lens=ODD) == -3
     assert call(B=0) == 0 and call(cap=24) == -1 and call(vc=None) == -1
+    assert call(w=ctypes.c_void_p(16 * 1000 + 4)) == -3 and call(o=ctypes.c_void_p(16 * 1000 + 8)) == -3
+    assert call(B=1 << 12, Hkv=1 << 10, Hq=1 << 10, cap=1 << 10) == -2          # more than 2^31 slots
 
 
 def test_key_weights_validation(lib):

@@ -9,8 +9,14 @@ Tolerances of the computed values, from the arithmetic:
   the base-2 constants), so a probability is off by a factor within ep = 2 ex +
   2^-18 (both numerator and denominator, the 2-ulp exponential, and sums of at
   most 2^5 serial steps per power of 2^-23);
-* o: the kernel rounds p * (scale of v) to bf16 once (2^-8) and its result to
-  bf16 (2^-8): |do| <= (2^-8 + ep) sum_j p |v| + 2^-8 |o|;
+* o: the kernel rounds p * (scale of v) once (to no less than bf16's 2^-8) and its
+  result to bf16 (2^-8).  The codes enter the product as c + 8 and -8 comes off 16
+  slots at a time: two matrix instructions, each a sum of 17 addends (16 products
+  and the accumulator) aligned to the largest and cut at 2^-24 of it, products up
+  to 15 p s (s: the scale).  What that adds is measured by the grid, not by the
+  value: 2 * 17 * 15 * 2^-24 < 2^-15 of p s, summed over the slots (a slot with
+  nearly all the probability and code 0 leaves 2^-15 s where another's tiny
+  share is the result).  So |do| <= (2^-8 + ep) sum_j p |v| + 2^-15 sum_j p s + 2^-8 |o|;
 * lse: |dl| <= ep + 2^-22 |lse|;
 * weights, per slot: <= w (ep + 2^-20) (sums of up to 16 heads in fp32; a prompt's
   weights are sums of positive terms over its queries, each partial sum of n terms
@@ -164,9 +170,9 @@ def run_decode(ta, q, dev, lens, scale, splits, weights=None):
 
 def check_decode(got, ref, d, what, w0=None):
     o, lse, w = (None if t is None else t.double().cpu().numpy() for t in got)
-    ro, rl, rw, pv, sm = ref
+    ro, rl, rw, pv, ps, sm = ref
     ep = 2 * (d + 16) * 2.0 ** -23 * sm + 2.0 ** -18
-    err = np.abs(o - ro) - ((2.0 ** -8 + ep[..., None]) * pv + 2.0 ** -8 * np.abs(ro))
+    err = np.abs(o - ro) - ((2.0 ** -8 + ep[..., None]) * pv + 2.0 ** -15 * ps + 2.0 ** -8 * np.abs(ro))
     assert (err <= 1e-30).all(), f"{what}: o off by {err.max():.3e} beyond its bound"
     empty = np.isneginf(rl)
     assert np.isneginf(lse[empty]).all(), what
@@ -237,6 +243,41 @@ def test_decode_scales_of_any_size(cuda_lib, d, mag):
     got = run_decode(cuda_lib, q.cuda(), dev, ints([93]), d ** -0.5, 2)
     ref = O.decode(q, host["kc"], host["ks"], host["vc"], host["vs"], [93], d ** -0.5)
     check_decode(got, ref, d, f"mag {mag}")
+
+
+def test_decode_many_sequences(cuda_lib):
+    """More sequences than a warp has lanes, most of them empty or tiny, one long."""
+    B, Hq, Hkv, cap, d = 77, 4, 2, 1008, 64
+    lens = [(7 * b) % 5 if b % 3 else 0 for b in range(B)]
+    lens[40], lens[76] = 1003, 65
+    host, dev = make_cache(B, Hkv, cap, d, 17)
+    q = torch.randn(B, Hq, 1, d, generator=torch.Generator().manual_seed(6)).bfloat16()
+    for splits in (1, 0, 1024):
+        w0 = torch.rand(B, Hkv, cap).cuda()
+        got = run_decode(cuda_lib, q.cuda(), dev, ints(lens), 0.2, splits, w0)
+        check_decode(got, O.decode(q, host["kc"], host["ks"], host["vc"], host["vs"], lens, 0.2), d, f"many {splits}", w0)
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """The last cache head of a cache of more than 2^32 bytes of codes: append, read, decode."""
+    ta = cuda_lib
+    B, Hkv, cap, d = 1, 36, 1 << 21, 128                      # 4.8 GB of codes each for K and V
+    c = ta.KV4Cache(B, Hkv, cap, d, track=False)
+    assert c.kc.numel() > 2 ** 32
+    g = torch.Generator().manual_seed(12)
+    k, v = (torch.randn(B, Hkv, 70, d, generator=g).bfloat16() for _ in range(2))
+    c.append(k.cuda(), v.cuda())
+    h = [0, Hkv - 1]
+    (kc, ks), (vc, vs) = O.quantize(k[:, h]), O.quantize(v[:, h])
+    assert np.array_equal(c.kc[:, h, :70].cpu().numpy(), O.pack(kc)) and np.array_equal(c.vc[:, h, :70].cpu().numpy(), O.pack(vc))
+    kr, _ = c.read(70)
+    assert same_values(kr[:, h], O.bf16_round((kc * np.repeat(ks, 32, axis=-1)).astype(np.float32)))
+    q = torch.randn(B, 2 * Hkv, 1, d, generator=g).bfloat16()
+    o, lse = ta.decode_kv4(q.cuda(), c, 0.1)
+    assert ta.attn_check_status() == 0
+    sel = [0, 1, 2 * Hkv - 2, 2 * Hkv - 1]
+    ref = O.decode(q[:, sel], O.pack(kc), ks, O.pack(vc), vs, [70], 0.1)
+    check_decode((o[:, sel], lse[:, sel], None), ref, d, "far offsets")
 
 
 def test_decode_nan_row_poisons_its_heads_only(cuda_lib):
@@ -388,7 +429,9 @@ def run_evict(ta, dev, w, pos, lens, nxt, n_keep, n_recent, alias=False):
     (1, 3, 2064, 64, [2050], 1024, 100, "random"), (2, 1, 1040, 128, [1025, 1030], 1024, 0, "ties"),
     (1, 2, 3008, 64, [3000], 17, 3, "ties"), (1, 1, 4000, 64, [4000], 3999, 64, "random"),
     (2, 2, 96, 64, [200, -3], 96, 0, "random"), (1, 2, 528, 64, [520], 300, 10, "special"), (1, 1, 160, 128, [150], 30, 30, "special"),
-    (1, 1, 40000, 64, [39990], 20000, 500, "random"),
+    (1, 1, 40000, 64, [39990], 20000, 500, "random"), (1, 2, 20000, 64, [19999], 9000, 40, "ties"),
+    (1, 1, 140000, 64, [139999], 70000, 1000, "random"), (1, 1, 135008, 128, [135001], 100, 7, "ties"),
+    (20, 8, 2064, 64, [2060 - b for b in range(20)], 1500, 64, "special"),
 ])
 def test_evict(cuda_lib, B, Hkv, cap, d, lens, n_keep, n_recent, kind, alias):
     g = torch.Generator().manual_seed(cap + n_keep)
@@ -420,6 +463,43 @@ def test_evict(cuda_lib, B, Hkv, cap, d, lens, n_keep, n_recent, kind, alias):
         assert torch.equal(got[..., :n_keep][live], given.gather(2, at)[live])
         if alias:
             assert torch.equal(got[..., n_keep:], given[..., n_keep:])
+
+
+def test_weights_and_eviction_in_a_graph(cuda_lib):
+    """Captured, replayed on other inputs: the same bits as the eager calls."""
+    ta = cuda_lib
+    g = torch.Generator().manual_seed(2)
+    B, Hq, Hkv, N, d, n_keep = 2, 4, 2, 700, 64, 300
+    q, k = (torch.randn(B, h, N, d, generator=g).bfloat16().cuda() for h in (Hq, Hkv))
+    _, lse = ta.forward(q, k, k, True)
+    c = ta.KV4Cache(B, Hkv, N, d)
+    c.append(k, k)
+    kept = torch.empty(B, Hkv, n_keep, dtype=torch.int32, device="cuda")
+    w_out, p_out = torch.zeros_like(c.weights), torch.zeros_like(c.positions)
+    ws = torch.empty(ta.attn_kv4_evict_workspace_bytes(B, Hkv, c.capacity, n_keep), dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(max(16, ta.attn_key_weights_workspace_bytes(B, Hq, Hkv, N, N, d)), dtype=torch.uint8, device="cuda")
+    qq = torch.zeros_like(q)
+
+    def call():
+        ta.attn_key_weights(qq, k, lse, c.weights, True, d ** -0.5, ws2)
+        ta.attn_kv4_evict(c.kc, c.ks, c.vc, c.vs, c.weights, c.positions, c.seqlens, c.next_pos, w_out, p_out, kept, 20, ws)
+    qq.copy_(q)
+    call()
+    first = [t.clone() for t in (c.weights, kept, w_out, p_out, c.kc, c.vs)]
+    qq.zero_()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    qq.copy_(q)
+    for t in (w_out, p_out, kept):
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ta.attn_check_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip((c.weights, kept, w_out, p_out, c.kc, c.vs), first))
 
 
 # ------------------------------------------------------------------ as they are used together

@@ -139,9 +139,11 @@ __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w;
 //     of the group, rounded to fp16 (the one rounding of P, 2^-11), with p
 //     taken times a power of two that keeps p s below 2^15.  That power follows
 //     the largest scale met so far as the running max follows the scores, so
-//     a product counts from 2^-31 of the largest on.  The offset goes out tile by
-//     tile through a second product with the constant -8: summed up over a long
-//     row it would swamp the result.
+//     a product counts from 2^-31 of the largest on.  The offset goes out 16
+//     slots at a time through a second product with the constant -8: summed up over
+//     a long row it would swamp the result.  What the cancellation leaves is below
+//     2^-15 of p times the scale (a step of the grid), far inside the format's own
+//     half step.
 template <int NG>
 __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS)
     decode_kv4_kernel(const __grid_constant__ DecKv4Params p) {
