@@ -433,10 +433,11 @@ static int launch_after(K kernel, unsigned grid, unsigned threads, cudaStream_t 
 template <int NG>
 static int launch_decode_kv4(const ta::DecKv4Params& p, attn_bf16_t* o, float* lse, float* weights, cudaStream_t st) {
   constexpr int D = 32 * NG, W = ta::KV4_FINISH_THREADS / 32;
-  const int rc = set_smem_attr(ta::decode_kv4_kernel<NG>, ta::DecKv4Cfg<NG>::SMEM);
+  const auto kernel = p.group <= 4 ? ta::decode_kv4_kernel<NG, true> : ta::decode_kv4_kernel<NG, false>;
+  const int rc = set_smem_attr(kernel, ta::DecKv4Cfg<NG>::SMEM);
   if (rc != ATTN_OK) return rc;
   const unsigned grid = (unsigned)((p.pieces + ta::KV4_WARPS - 1) / ta::KV4_WARPS);
-  ta::decode_kv4_kernel<NG><<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<NG>::SMEM, st>>>(p);
+  kernel<<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<NG>::SMEM, st>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   const long long rows = (long long)p.B * p.Hkv * p.group, heads = (long long)p.B * p.Hkv;
   const bool wide = p.pieces >= 8 * heads * p.blocks;

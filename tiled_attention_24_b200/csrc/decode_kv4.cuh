@@ -43,9 +43,9 @@ struct DecKv4Params {
 // A tile of 64 slots is one straight run of instructions: with 2 warps on each
 // scheduler and up to 255 registers the independent chains of its four 16-slot
 // parts hide the latencies better than more warps do with shorter runs (64
-// sequences of 8192 slots, 8 cache heads of 4 query heads, 605 MB: 148 us; 12 warps
-// of 168 registers and 32 slots 161; 16 warps of 128 and 32 slots 159; 16 slots
-// at a time 169 to 178).
+// sequences of 8192 slots, 8 cache heads of 4 query heads, 605 MB, at the time: 148 us;
+// 12 warps of 168 registers and 32 slots 161; 16 warps of 128 and 32 slots 159; 16
+// slots at a time 169 to 178).
 constexpr int KV4_TILE = 64;                // slots of a tile
 constexpr int KV4_WARPS = 4, KV4_CTAS = 2;  // warps of a CTA, CTAs of an SM
 
@@ -116,6 +116,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ float bf2f(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16)); }
 
+// half of a word of scales as a float, by a byte selector (0x1044 the low one, 0x3244 the high one)
+__device__ __forceinline__ float kv4_half_float(uint32_t w, uint32_t pick) {
+  return __uint_as_float(__byte_perm(w, 0u, pick));
+}
 // word i (two groups) of a row's scales
 __device__ __forceinline__ uint32_t kv4_word(const uint2& w, int i) { return i ? w.y : w.x; }
 __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w; }
@@ -144,7 +148,14 @@ __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w;
 //     a long row it would swamp the result.  What the cancellation leaves is below
 //     2^-15 of p times the scale (a step of the grid), far inside the format's own
 //     half step.
-template <int NG>
+//
+// PAIR, for up to 4 heads: the 8 columns are 4 heads for the even and 4 heads for
+// the odd group of a pair.  A word of codes (4 channels of each group of the pair)
+// then is an operand as it lies, without bringing a group's halves together, a
+// lane works on the scales of one group of the pair only, and one more addition
+// across lanes joins the scores of the two (64 x 8192 slots, 8 cache heads of 4:
+// 141 us against 143, one row of 131072 slots 53 against 55).
+template <int NG, bool PAIR>
 __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS)
     decode_kv4_kernel(const __grid_constant__ DecKv4Params p) {
   using C = DecKv4Cfg<NG>;
@@ -245,16 +256,19 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     const int bhk = at.item / p.blocks, blk = at.item - bhk * p.blocks;
     const int heads = min(8, p.group - blk * 8);
     const size_t bh0 = (size_t)bhk * p.group + blk * 8;  // first query head (batch * Hq + head)
-  // ---- queries: head r, channels 32 g + 8 t + 0..7 of each group, as B fragments
-  uint32_t qb[NG][4];
-  float c0[NG][4];  // accumulator start of heads 2t, 2t + 1, once for each slot of the lane
+  // ---- queries: head r, channels 32 g + 8 t + 0..7 of each group, as B fragments.
+  // PAIR: head r % 4, of each pair of groups the even (r < 4) or the odd one
+  constexpr int NQ = PAIR ? NG / 2 : NG;
+  const int head = PAIR ? r & 3 : r, hi = t >> 1;  // hi: this lane's scores are the odd group's
+  uint32_t qb[NQ][PAIR ? 8 : 4];
+  float c0[NQ][4];  // accumulator start of heads 2t, 2t + 1, once for each slot of the lane
   float fx[2];
   {
     uint4 w[NG];
     uint32_t m = 0;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      w[g] = r < heads ? *reinterpret_cast<const uint4*>(p.q + (bh0 + r) * D + 32 * g + 8 * t) : make_uint4(0, 0, 0, 0);
+      w[g] = head < heads ? *reinterpret_cast<const uint4*>(p.q + (bh0 + head) * D + 32 * g + 8 * t) : make_uint4(0, 0, 0, 0);
       const uint32_t a = __vmaxu2(__vmaxu2(w[g].x & 0x7FFF7FFFu, w[g].y & 0x7FFF7FFFu),
                                   __vmaxu2(w[g].z & 0x7FFF7FFFu, w[g].w & 0x7FFF7FFFu));
       m = max(m, max(a & 0xFFFFu, a >> 16));
@@ -267,8 +281,9 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     const int e0 = (14 - e) / 2;  // 2^(14 - e) in two factors
     const float up0 = __uint_as_float((uint32_t)(127 + e0) << 23), up1 = __uint_as_float((uint32_t)(127 + 14 - e - e0) << 23);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const uint32_t ww[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+    for (int g = 0; g < NQ; ++g) {
+      const uint4 own = !PAIR ? w[g] : r < 4 ? w[2 * g] : w[2 * g + 1 < NG ? 2 * g + 1 : 0];
+      const uint32_t ww[4] = {own.x, own.y, own.z, own.w};
       float f[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -276,11 +291,20 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         f[2 * k + 1] = bf2f(ww[k], 1) * up0 * (up1 * 0.0625f);
       }
       float sum = 0.f;
+      if constexpr (PAIR) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // nibble k of the two halfwords: channels k and 4 + k
+        for (int k = 0; k < 8; ++k) {  // channel k: nibble k % 4 of piece 2t or 2t + 1
+          const __half2 h = r < 4 ? __floats2half2_rn(f[k], 0.f) : __floats2half2_rn(0.f, f[k]);
+          qb[g][k] = *reinterpret_cast<const uint32_t*>(&h);
+          sum += (__low2float(h) + __high2float(h)) * ((k & 1) ? 16.f : 1.f);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // nibble k of the two halfwords: channels k and 4 + k
         const __half2 h = __floats2half2_rn(f[k], f[4 + k]);
         qb[g][k] = *reinterpret_cast<const uint32_t*>(&h);
         sum += (__low2float(h) + __high2float(h)) * ((k & 1) ? 16.f : 1.f);
+      }
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -309,6 +333,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   int ev = -100;
   uint32_t vref = (uint32_t)((127 - 100) << 7) * 0x10001u;
   const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
+  const uint32_t pick = hi ? 0x3244u : 0x1044u;  // PAIR: this lane's half of a word of scales, as a float
 
   for (const int end = min(mine, i + at.tiles - at.tile); i < end; ++i, ++at.tile) {
     ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars[st]), phase, abort_flag, p.timeout_ns));
@@ -321,6 +346,48 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     float y[C::U][4];
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
+      if constexpr (PAIR) {
+        uint32_t kw[2][NG];
+        T sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = 16 * u + r + 8 * h;
+          if constexpr (NG == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(buf + row * 64 + t * 16);
+            kw[h][0] = w.x, kw[h][1] = w.z, kw[h][2] = w.y, kw[h][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(buf + row * 32 + t * 8);
+            kw[h][0] = w.x, kw[h][1] = w.y;
+          }
+          sc[h] = *reinterpret_cast<const T*>(ksb + row * NG * 2);
+        }
+#pragma unroll
+        for (int g = 0; g < NQ; ++g) {
+          float s[4];
+#pragma unroll
+          for (int piece = 0; piece < 2; ++piece) {
+            const uint32_t a = kw[0][2 * g + piece], b = kw[1][2 * g + piece], a8 = a >> 8, b8 = b >> 8;
+            const uint32_t* q4 = &qb[g][4 * piece];
+            if (piece == 0)
+              mma_f16_16816(s, and_xor<0x000F000Fu>(a, flip0), and_xor<0x000F000Fu>(b, flip0),
+                            and_xor<0x00F000F0u>(a, flip1), and_xor<0x00F000F0u>(b, flip1), q4[0], q4[1], c0[g][0],
+                            c0[g][1], c0[g][2], c0[g][3]);
+            else
+              mma_f16_16816(s, and_xor<0x000F000Fu>(a, flip0), and_xor<0x000F000Fu>(b, flip0),
+                            and_xor<0x00F000F0u>(a, flip1), and_xor<0x00F000F0u>(b, flip1), q4[0], q4[1]);
+            mma_f16_16816(s, and_xor<0x000F000Fu>(a8, flip0), and_xor<0x000F000Fu>(b8, flip0),
+                          and_xor<0x00F000F0u>(a8, flip1), and_xor<0x00F000F0u>(b8, flip1), q4[2], q4[3]);
+          }
+          const float f0 = kv4_half_float(kv4_word(sc[0], g), pick), f1 = kv4_half_float(kv4_word(sc[1], g), pick);
+          y[u][0] = g ? fmaf(s[0], f0, y[u][0]) : s[0] * f0;
+          y[u][1] = g ? fmaf(s[1], f0, y[u][1]) : s[1] * f0;
+          y[u][2] = g ? fmaf(s[2], f1, y[u][2]) : s[2] * f1;
+          y[u][3] = g ? fmaf(s[3], f1, y[u][3]) : s[3] * f1;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[u][e] += __shfl_xor_sync(0xffffffffu, y[u][e], 2);
+        continue;
+      }
       uint32_t kw[2][NG];
       T sc[2];
 #pragma unroll
@@ -337,7 +404,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         sc[h] = *reinterpret_cast<const T*>(ksb + row * NG * 2);
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int g = 0; g < (PAIR ? 0 : NG); ++g) {
         float s[4];
         const uint32_t a = kw[0][g], b = kw[1][g], a8 = a >> 8, b8 = b >> 8;
         mma_f16_16816(s, and_xor<0x000F000Fu>(a, flip0), and_xor<0x000F000Fu>(b, flip0),
@@ -429,8 +496,36 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
       for (int h = 0; h < 4; ++h)
         vw[h] = *reinterpret_cast<const T*>(buf + C::CODES + (16 * u + 2 * t + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * 2 * NG);
+      if constexpr (PAIR) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NQ; ++g) {
+          const float f0 = kv4_half_float(kv4_word(vs[u][0], g), pick), f1 = kv4_half_float(kv4_word(vs[u][1], g), pick);
+          const uint32_t b0 = movmatrix_trans(pack_f16(pr[u][0] * f0, pr[u][1] * f0));
+          const uint32_t b1 = movmatrix_trans(pack_f16(pr[u][2] * f1, pr[u][3] * f1));
+          uint32_t a[4];  // even and odd group: slots 2t, 2t + 1, then 2t + 8, 2t + 9
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            a[h] = __byte_perm(kv4_word(vw[h & 2], g), kv4_word(vw[(h & 2) + 1], g), (h & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (n == 1) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) a[h] >>= 8;
+            }
+            float(&o0)[4] = acc[4 * g + 2 * n];
+            float(&o1)[4] = acc[4 * g + 2 * n + 1];
+            mma_f16_16816(o0, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
+            mma_f16_16816(o1, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, b0, b1);
+            mma_f16_16816(o0, and_xor<0x000F000Fu>(a[0], flip0), and_xor<0x000F000Fu>(a[1], flip0),
+                          and_xor<0x000F000Fu>(a[2], flip0), and_xor<0x000F000Fu>(a[3], flip0), b0, b1);
+            mma_f16_16816(o1, and_xor<0x00F000F0u>(a[0], flip1), and_xor<0x00F000F0u>(a[1], flip1),
+                          and_xor<0x00F000F0u>(a[2], flip1), and_xor<0x00F000F0u>(a[3], flip1), b0, b1);
+          }
+        }
+        continue;
+      }
+#pragma unroll
+      for (int g = 0; g < (PAIR ? 0 : NG); ++g) {
         const float f0 = bf2f(kv4_word(vs[u][0], g >> 1), g & 1), f1 = bf2f(kv4_word(vs[u][1], g >> 1), g & 1);
         const uint32_t b0 = movmatrix_trans(pack_f16(pr[u][0] * f0, pr[u][1] * f0));
         const uint32_t b1 = movmatrix_trans(pack_f16(pr[u][2] * f1, pr[u][3] * f1));
@@ -460,8 +555,25 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
   const size_t part = (size_t)(piece + at.item) * p.per_block;  // unique: the next piece or item has the next number
+  if constexpr (PAIR) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 2; ++k) {
+      const int h = (2 * t + k) & 3;
+      if (h >= heads) continue;
+      float* o = p.o_part + (part + h) * D + 32 * hi + 4 * r;
+#pragma unroll
+      for (int g = 0; g < NQ; ++g) {
+        float v[4];
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4)  // odd nibbles carry 16
+          v[i4] = (hi ? acc[4 * g + i4][k + 2] : acc[4 * g + i4][k]) * ((i4 & 1) ? 0x1p20f : 0x1p24f);
+        *reinterpret_cast<float4*>(o + 64 * g) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      if (r == 0 && !hi) p.ml_part[part + h] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < (PAIR ? 0 : 2); ++k) {
     if (2 * t + k >= heads) continue;
     float* o = p.o_part + (part + 2 * t + k) * D + 4 * r;
 #pragma unroll
