@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   if (mine == 0) return;
   const int piece = blockIdx.x * C::WARPS + warp;
   int b = 0, before = 0;  // batch entry of the first tile, tiles before it
-  for (int b0 = 0;; b0 += 32) {
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int n = b0 + lane < p.B ? kv4_tiles(p.seqlens, b0 + lane, p.cap) * per_entry : 0;
     int sum = n;
 #pragma unroll
