@@ -261,8 +261,8 @@ constexpr int KV4_EVICT_BINS = 2048;
 struct Kv4EvictShared {
   int hist[KV4_EVICT_BINS];   // this CTA's
   int total[KV4_EVICT_BINS];  // the cluster's, in its first CTA
-  int warp[2][KV4_EVICT_WARPS];
-  int cta[3][8];              // per CTA: equal keys, holes, sources
+  int2 warp[2][KV4_EVICT_WARPS];
+  int2 cta[2][8];             // per CTA: equal keys; holes and sources
   uint32_t prefix;
   int need, ties;  // of the keys that match the prefix: to be kept, in all
 };
@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
         const int v = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += v;
       }
-      if (lane == 31) sh.warp[0][warp] = before;
+      if (lane == 31) sh.warp[0][warp].x = before;
       __syncthreads();
-      for (int k = 0; k < warp; ++k) before += sh.warp[0][k];
+      for (int k = 0; k < warp; ++k) before += sh.warp[0][k].x;
       before -= sum;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
@@ -382,85 +382,90 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
     mask |= digits << shift;
   }
 
-  // ---- 2. who stays
+  // ---- 2. who stays: a bit for each slot
   const int run = slice / KV4_EVICT_WARPS, i0 = warp * run, i1 = min(i0 + run, n);
-  // sums over lower warps and CTAs of a per-warp count (lane 0's); the cluster's total
-  auto before_me = [&](int count, int which, int& total) {
-    if (lane == 0) sh.warp[which & 1][warp] = count;
+  // exclusive sums over lower threads and CTAs of two per-thread counts; the cluster's totals
+  auto before_me = [&](int2 c, int which, int2& total) {
+    int2 up = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, up.x, o), y = __shfl_up_sync(0xffffffffu, up.y, o);
+      if (lane >= o) up.x += x, up.y += y;
+    }
+    if (lane == 31) sh.warp[which][warp] = up;
     __syncthreads();
-    int before = 0, mine = 0;
+    int2 before = make_int2(up.x - c.x, up.y - c.y), mine = make_int2(0, 0);
     for (int k = 0; k < KV4_EVICT_WARPS; ++k) {
-      if (k < warp) before += sh.warp[which & 1][k];
-      mine += sh.warp[which & 1][k];
+      const int2 v = sh.warp[which][k];
+      if (k < warp) before.x += v.x, before.y += v.y;
+      mine.x += v.x, mine.y += v.y;
     }
     if (tid < CL) cluster.map_shared_rank(&sh.cta[which][0], tid)[rank] = mine;
     cluster.sync();
-    total = 0;
+    total = make_int2(0, 0);
     for (int r = 0; r < CL; ++r) {
-      if (r < rank) before += sh.cta[which][r];
-      total += sh.cta[which][r];
+      const int2 v = sh.cta[which][r];
+      if (r < rank) before.x += v.x, before.y += v.y;
+      total.x += v.x, total.y += v.y;
     }
     return before;
   };
-  int eq = 0, all;
+  int2 all;
   if (sh.ties > need) {  // some of the equal keys go: which, by their order
     int count = 0;
     for (int i = i0; i < i1; i += 32)
       count += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && key_at(i + lane) == prefix));
-    eq = before_me(count, 0, all);
+    int eq = __shfl_sync(0xffffffffu, before_me(make_int2(lane == 0 ? count : 0, 0), 0, all).x, 0);
+    for (int i = i0; i < i1; i += 32) {
+      const bool in = i + lane < i1;
+      const uint32_t key = in ? key_at(i + lane) : 0u;
+      const unsigned same = __ballot_sync(0xffffffffu, in && key == prefix);
+      const bool stays = in && (key > prefix || (key == prefix && eq + __popc(same & ((1u << lane) - 1u)) < need));
+      const unsigned keep = __ballot_sync(0xffffffffu, stays);
+      eq += __popc(same);
+      if (lane == 0) keep_bits[i / 32] = keep;
+    }
   } else {
-    need = 0x7fffffff;
-  }
-  int holes = 0, sources = 0;
 #pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    const unsigned same = __ballot_sync(0xffffffffu, in && key == prefix);
-    const bool stays = in && (key > prefix || (key == prefix && eq + __popc(same & ((1u << lane) - 1u)) < need));
-    const unsigned keep = __ballot_sync(0xffffffffu, stays);
-    eq += __popc(same);
-    if (lane == 0) keep_bits[i / 32] = keep;
-    const int j = j0 + i + lane;
-    holes += __popc(__ballot_sync(0xffffffffu, in && !stays && j < p.n_keep));
-    sources += __popc(__ballot_sync(0xffffffffu, stays && j >= p.n_keep));
+    for (int i = i0; i < i1; i += 32) {
+      const unsigned keep = __ballot_sync(0xffffffffu, i + lane < i1 && key_at(i + lane) >= prefix);
+      if (lane == 0) keep_bits[i / 32] = keep;
+    }
   }
-  int moves;
-  holes = before_me(holes, 1, moves);
-  sources = before_me(sources, 2, all);
+  __syncthreads();
 
-  // ---- 3. the lists, then the rows
+  // ---- 3. the lists, then the rows.  A thread has `words` words of 32 slots
   int* hole_list = p.lists + (size_t)bh * 2 * p.n_keep;
   int* source_list = hole_list + p.n_keep;
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const unsigned keep = keep_bits[i / 32], below = (1u << lane) - 1u;
-    const int j = j0 + i + lane;
-    const bool in = i + lane < i1, stays = (keep >> lane) & 1u, front = j < p.n_keep;
-    const unsigned h = __ballot_sync(0xffffffffu, in && !stays && front);
-    const unsigned s = __ballot_sync(0xffffffffu, in && stays && !front);
-    if ((h >> lane) & 1u) hole_list[holes + __popc(h & below)] = j;
-    if ((s >> lane) & 1u) source_list[sources + __popc(s & below)] = j;
-    holes += __popc(h);
-    sources += __popc(s);
-    if (in && stays && front) kept[j] = j;
+  const int words = (slice / 32 + KV4_EVICT_THREADS - 1) / KV4_EVICT_THREADS, w0 = tid * words;
+  auto low = [](int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };  // bits [0, k)
+  auto hole_bits = [&](int k) { return 32 * k < n ? ~keep_bits[k] & low(n - 32 * k) & low(p.n_keep - j0 - 32 * k) : 0u; };
+  auto source_bits = [&](int k) { return 32 * k < n ? keep_bits[k] & ~low(p.n_keep - j0 - 32 * k) : 0u; };
+  int2 count = make_int2(0, 0);
+  for (int k = w0; k < w0 + words; ++k) count.x += __popc(hole_bits(k)), count.y += __popc(source_bits(k));
+  int2 at = before_me(count, 1, all);
+  const int moves = all.x;
+  for (int k = w0; k < w0 + words; ++k) {
+    for (unsigned m = hole_bits(k); m; m &= m - 1) hole_list[at.x++] = j0 + 32 * k + __ffs(m) - 1;
+    for (unsigned m = source_bits(k); m; m &= m - 1) source_list[at.y++] = j0 + 32 * k + __ffs(m) - 1;
   }
-  __syncthreads();  // keep_bits of other warps
-  if (w_out != w || pos_out != pos) {
-    const int front = min(n, p.n_keep - j0);
-    for (int i = tid; i < front; i += 8 * KV4_EVICT_THREADS) {  // 8 slots a thread in flight
-      float a[8];
-      int c[8];
+  const int front = min(n, p.n_keep - j0);
+  const bool copy = w_out != w || pos_out != pos;
+  for (int i = tid; i < front; i += 8 * KV4_EVICT_THREADS) {  // 8 slots a thread in flight
+    float a[8];
+    int c[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = i + k * KV4_EVICT_THREADS;
-        a[k] = at < front ? w[j0 + at] : 0.f;
-        c[k] = at < front ? pos[j0 + at] : 0;
-      }
+    for (int k = 0; k < 8; ++k) {
+      const int s = i + k * KV4_EVICT_THREADS;
+      a[k] = copy && s < front ? w[j0 + s] : 0.f;
+      c[k] = copy && s < front ? pos[j0 + s] : 0;
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = i + k * KV4_EVICT_THREADS;
-        if (at < front && ((keep_bits[at / 32] >> lane) & 1u)) w_out[j0 + at] = a[k], pos_out[j0 + at] = c[k];
+    for (int k = 0; k < 8; ++k) {
+      const int s = i + k * KV4_EVICT_THREADS;
+      if (s < front && ((keep_bits[s / 32] >> lane) & 1u)) {
+        kept[j0 + s] = j0 + s;
+        if (copy) w_out[j0 + s] = a[k], pos_out[j0 + s] = c[k];
       }
     }
   }
