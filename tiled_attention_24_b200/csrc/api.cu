@@ -440,14 +440,18 @@ static int launch_decode_kv4(const ta::DecKv4Params& p, attn_bf16_t* o, float* l
   kernel<<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<NG>::SMEM, st>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   const long long rows = (long long)p.B * p.Hkv * p.group, heads = (long long)p.B * p.Hkv;
-  const bool wide = p.pieces >= 8 * heads * p.blocks;
-  const long long merge = wide ? rows * NG : (rows + W - 1) / W;
+  // Partials a row, were the sequences alike.  A warp takes 8 in one chain of loads, a
+  // CTA 8 (d = 64: 16) beside one another; over 64 there are few rows, and a CTA
+  // takes 32 channels of one.
+  const long long parts = p.pieces / (heads * p.blocks);
+  const int ctas = parts <= 8 ? 0 : parts < 64 ? 1 : NG;
+  const long long merge = ctas ? rows * ctas : (rows + W - 1) / W;
   const long long more = weights ? heads * ((p.cap + ta::KV4_FINISH_SLOTS - 1) / ta::KV4_FINISH_SLOTS) : 0;
   if (merge + more > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-  return wide ? launch_after(ta::decode_kv4_finish_kernel<D, true>, (unsigned)(merge + more), ta::KV4_FINISH_THREADS, st,
-                             p, o, lse, weights, (int)merge)
-              : launch_after(ta::decode_kv4_finish_kernel<D, false>, (unsigned)(merge + more), ta::KV4_FINISH_THREADS,
-                             st, p, o, lse, weights, (int)merge);
+  const auto finish = ctas == 0   ? ta::decode_kv4_finish_kernel<D, 0>
+                      : ctas == 1 ? ta::decode_kv4_finish_kernel<D, 1>
+                                  : ta::decode_kv4_finish_kernel<D, NG>;
+  return launch_after(finish, (unsigned)(merge + more), ta::KV4_FINISH_THREADS, st, p, o, lse, weights, (int)merge);
 }
 
 // One cluster per (batch, cache head), of 1 to 8 CTAs: as many as fill the 296 that

@@ -607,88 +607,110 @@ __device__ __forceinline__ Kv4Parts kv4_row_parts(const DecKv4Params& p, int row
   r.n = tiles == 0 ? 0 : (t0 + tiles - 1) / per - c0 + 1;
   return r;
 }
-// max of the partials' exponents and log2 sum_c 2^(M_c - max) l_c; whole warp
-__device__ __forceinline__ float kv4_parts_max(const float2* ml, int step, int n) {
-  float mx = -INFINITY;
-  for (int c = threadIdx.x & 31; c < n; c += 32) mx = fmaxf(mx, ml[(size_t)c * step].x);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-  return mx;
-}
 __device__ __forceinline__ float kv4_part_factor(float M, float mx) { return M == mx ? 1.f : ex2(M - mx); }  // all NaN: no max
 __device__ __forceinline__ float kv4_lse2(float mx, float l) { return (mx == -INFINITY ? 0.f : mx) + log2f(l); }
+__device__ __forceinline__ float kv4_warp_max(float v) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+  return v;
+}
+// max M + log2 sum_c 2^(M_c - max M) l_c over a row's partials; whole warp
+__device__ __forceinline__ float kv4_row_lse2(const DecKv4Params& p, const Kv4Parts& parts) {
+  const float2* ml = p.ml_part + parts.first;
+  float m = -INFINITY, l = 0.f;
+  for (int c = threadIdx.x & 31; c < parts.n; c += 32) {
+    const float2 v = ml[(size_t)c * p.per_block];
+    const float grown = fmaxf(m, v.x);
+    l = fmaf(l, kv4_part_factor(m, grown), kv4_part_factor(v.x, grown) * v.y);
+    m = grown;
+  }
+  const float mx = kv4_warp_max(m);
+  l *= kv4_part_factor(m, mx);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  return kv4_lse2(mx, l);
+}
 
 // What the pieces left becomes the outputs, in one launch.  The first CTAs merge: with
 // f = 2^(M_c - max M), O = sum f O_c / sum f l_c, LSE = ln 2 (max M + log2 sum f l_c);
-// a row without slots has no partial, a NaN in a live slot stays one.  WIDE (8
-// partials a row or more): a CTA per row and 32 channels, 32 partials at a time;
-// else a warp per row.  The other CTAs, where weights are wanted, take 1024
-// slots of a cache head each: w_j += sum_h 2^(x_hj - lse_h log2 e), with the rows'
-// log-sum-exps worked out again from the partials' (M, l), a few KB.
-constexpr int KV4_FINISH_THREADS = 256, KV4_FINISH_SLOTS = 4 * KV4_FINISH_THREADS, KV4_FINISH_HEADS = 64;
-template <int D, bool WIDE>
+// a row without slots has no partial, a NaN in a live slot stays one.  CTAS = 0: a
+// warp per row, its partials in loads of 8; 1: a CTA per row, a warp (half a warp of
+// d = 64) per partial; more: a CTA per 32 channels of a row, 32 partials at a time.
+// The other CTAs, where weights are wanted, take 1024 slots of a cache head each:
+// w_j += sum_h 2^(x_hj - lse_h log2 e), with the rows' log-sum-exps worked out again
+// from the partials' (M, l), a few KB.  Every chain of loads costs about 1 us, so
+// each is begun before the one it does not need: places from the lengths before the
+// wait for the pieces, scores and partials before the maxima.
+constexpr int KV4_FINISH_THREADS = 256, KV4_FINISH_SLOTS = 4 * KV4_FINISH_THREADS;
+constexpr int KV4_FINISH_WARPS = KV4_FINISH_THREADS / 32;
+template <int D, int CTAS>
 __global__ void __launch_bounds__(KV4_FINISH_THREADS)
     decode_kv4_finish_kernel(const __grid_constant__ DecKv4Params p, uint16_t* __restrict__ o, float* __restrict__ lse,
                              float* __restrict__ weights, int merge_blocks) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((int)blockIdx.x >= merge_blocks) {
-    // ---- weights
-    __shared__ float s_lse2[KV4_FINISH_HEADS];
+    // ---- weights; a warp finds a head's log-sum-exp, 8 heads at a time
+    __shared__ float s_lse2[KV4_FINISH_WARPS];
     const int per = (p.cap + KV4_FINISH_SLOTS - 1) / KV4_FINISH_SLOTS, at = blockIdx.x - merge_blocks;
     const int bhk = at / per, j = (at - bhk * per) * KV4_FINISH_SLOTS + 4 * tid;
     const int len = min(max(p.seqlens[bhk / p.Hkv], 0), p.cap);
+    const bool any = j - 4 * tid < len;
+    Kv4Parts parts = {0, 0};
+    if (any && warp < p.group) parts = kv4_row_parts(p, bhk * p.group + warp);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (j - 4 * tid >= len) return;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int h0 = 0; h0 < p.group; h0 += KV4_FINISH_HEADS) {
-      const int heads = min(KV4_FINISH_HEADS, p.group - h0);
-      __syncthreads();
-      for (int h = warp; h < heads; h += KV4_FINISH_THREADS / 32) {
-        const Kv4Parts parts = kv4_row_parts(p, bhk * p.group + h0 + h);
-        const float2* ml = p.ml_part + parts.first;
-        const float mx = kv4_parts_max(ml, p.per_block, parts.n);
-        float l = 0.f;
-        for (int c = lane; c < parts.n; c += 32) {
-          const float2 v = ml[(size_t)c * p.per_block];
-          l = fmaf(kv4_part_factor(v.x, mx), v.y, l);
-        }
+    if (!any) return;
+    const float* x = p.x + (size_t)bhk * p.group * p.cap + j;
+    float4* w4 = reinterpret_cast<float4*>(weights + (size_t)bhk * p.cap + j);  // j, capacity: multiples of 4
+    float4 old = make_float4(0.f, 0.f, 0.f, 0.f), sum = old;
+    if (j < len) old = *w4;
+    float4 v[4];
+    const auto load = [&](int h0) {
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-        if (lane == 0) s_lse2[h] = kv4_lse2(mx, l);
-      }
-      __syncthreads();
-      if (j < len) {
-        const float* x = p.x + ((size_t)bhk * p.group + h0) * p.cap + j;
-#pragma unroll 4
-        for (int h = 0; h < heads; ++h) {
-          const float4 v = *reinterpret_cast<const float4*>(x + (size_t)h * p.cap);
-          const float l2 = s_lse2[h];
-          sum.x += ex2(v.x - l2), sum.y += ex2(v.y - l2), sum.z += ex2(v.z - l2), sum.w += ex2(v.w - l2);
+      for (int h = 0; h < 4; ++h)
+        if (h0 + h < p.group && j < len) v[h] = *reinterpret_cast<const float4*>(x + (size_t)(h0 + h) * p.cap);
+    };
+    load(0);
+    for (int h0 = 0; h0 < p.group; h0 += 4) {
+      if (h0 % KV4_FINISH_WARPS == 0) {
+        if (h0 > 0) {
+          __syncthreads();
+          if (h0 + warp < p.group) parts = kv4_row_parts(p, bhk * p.group + h0 + warp);
         }
+        if (h0 + warp < p.group) {
+          const float l2 = kv4_row_lse2(p, parts);
+          if (lane == 0) s_lse2[warp] = l2;
+        }
+        __syncthreads();
       }
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (h0 + h < p.group && j < len) {
+          const float l2 = s_lse2[(h0 + h) % KV4_FINISH_WARPS];
+          sum.x += ex2(v[h].x - l2), sum.y += ex2(v[h].y - l2), sum.z += ex2(v[h].z - l2), sum.w += ex2(v[h].w - l2);
+        }
+      load(h0 + 4);
     }
-    float* w = weights + (size_t)bhk * p.cap + j;
+    old.x += sum.x, old.y += sum.y, old.z += sum.z, old.w += sum.w;
     if (j + 4 <= len) {
-      float4 v = *reinterpret_cast<float4*>(w);
-      v.x += sum.x, v.y += sum.y, v.z += sum.z, v.w += sum.w;
-      *reinterpret_cast<float4*>(w) = v;
+      *w4 = old;
     } else if (j < len) {
-      w[0] += sum.x;
-      if (j + 1 < len) w[1] += sum.y;
-      if (j + 2 < len) w[2] += sum.z;
+      float* w = reinterpret_cast<float*>(w4);
+      w[0] = old.x;
+      if (j + 1 < len) w[1] = old.y;
+      if (j + 2 < len) w[2] = old.z;
     }
     return;
   }
   // ---- merge
-  constexpr int LANES = WIDE ? 8 : D / 4;  // float4 of channels
-  constexpr int GROUPS = (WIDE ? KV4_FINISH_THREADS : 32) / LANES;
-  const int row = WIDE ? blockIdx.x / (D / 32) : blockIdx.x * (KV4_FINISH_THREADS / 32) + warp;
-  const int first = WIDE ? blockIdx.x % (D / 32) * 8 : 0;
+  constexpr int LANES = CTAS > 1 ? 8 : D / 4;  // float4 of channels
+  constexpr int GROUPS = (CTAS ? KV4_FINISH_THREADS : 32) / LANES, BATCH = 4;
+  const int row = CTAS ? blockIdx.x / (CTAS ? CTAS : 1) : blockIdx.x * KV4_FINISH_WARPS + warp;
+  const int first = CTAS > 1 ? blockIdx.x % (CTAS ? CTAS : 1) * 8 : 0;
   if (row >= p.B * p.Hkv * p.group) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // this grid never ends before the one it follows
     return;
   }
-  const int lane4 = (WIDE ? tid : lane) % LANES, grp = (WIDE ? tid : lane) / LANES;
+  const int lane4 = (CTAS ? tid : lane) % LANES, grp = (CTAS ? tid : lane) / LANES;
   uint2* out = reinterpret_cast<uint2*>(o + (size_t)row * D) + first + lane4;
   const Kv4Parts parts = kv4_row_parts(p, row);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -698,16 +720,29 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
     return;
   }
   const float2* ml = p.ml_part + parts.first;
-  const float mx = kv4_parts_max(ml, p.per_block, parts.n);
+  const float4* op = reinterpret_cast<const float4*>(p.o_part + parts.first * D) + first + lane4;
+  const int o_step = p.per_block * (D / 4);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int c = grp; c < parts.n; c += GROUPS) {
-    const float2 v = ml[(size_t)c * p.per_block];
-    const float4 w = reinterpret_cast<const float4*>(p.o_part + (parts.first + (size_t)c * p.per_block) * D)[first + lane4];
-    const float f = kv4_part_factor(v.x, mx);
-    l = fmaf(f, v.y, l);
-    a.x = fmaf(f, w.x, a.x), a.y = fmaf(f, w.y, a.y), a.z = fmaf(f, w.z, a.z), a.w = fmaf(f, w.w, a.w);
+  float l = 0.f, mx = -INFINITY;
+  for (int c0 = 0; c0 < parts.n; c0 += BATCH * GROUPS) {
+    float2 v[BATCH];
+    float4 w[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int c = c0 + k * GROUPS + grp;
+      if (c < parts.n) v[k] = ml[(size_t)c * p.per_block], w[k] = op[(size_t)c * o_step];
+    }
+    if (c0 == 0) {
+      for (int c = lane; c < parts.n; c += 32) mx = fmaxf(mx, ml[(size_t)c * p.per_block].x);
+      mx = kv4_warp_max(mx);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (c0 + k * GROUPS + grp >= parts.n) break;
+      const float f = kv4_part_factor(v[k].x, mx);
+      l = fmaf(f, v[k].y, l);
+      a.x = fmaf(f, w[k].x, a.x), a.y = fmaf(f, w[k].y, a.y), a.z = fmaf(f, w[k].z, a.z), a.w = fmaf(f, w[k].w, a.w);
+    }
   }
 #pragma unroll
   for (int k = LANES; k < 32; k <<= 1) {
@@ -715,17 +750,17 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
     a.z += __shfl_xor_sync(0xffffffffu, a.z, k), a.w += __shfl_xor_sync(0xffffffffu, a.w, k);
     l += __shfl_xor_sync(0xffffffffu, l, k);
   }
-  if (WIDE) {
-    __shared__ float4 s_o[KV4_FINISH_THREADS / 32][8];
-    __shared__ float s_l[KV4_FINISH_THREADS / 32];
-    if (lane < 8) s_o[warp][lane] = a;
+  if (CTAS) {
+    __shared__ float4 s_o[KV4_FINISH_WARPS][LANES];
+    __shared__ float s_l[KV4_FINISH_WARPS];
+    if (lane < LANES) s_o[warp][lane] = a;
     if (lane == 0) s_l[warp] = l;
     __syncthreads();
-    if (tid >= 8) return;
+    if (tid >= LANES) return;
     a = make_float4(0.f, 0.f, 0.f, 0.f);
     l = 0.f;
 #pragma unroll
-    for (int k = 0; k < KV4_FINISH_THREADS / 32; ++k) {
+    for (int k = 0; k < KV4_FINISH_WARPS; ++k) {
       const float4 w = s_o[k][tid];
       a.x += w.x, a.y += w.y, a.z += w.z, a.w += w.w;
       l += s_l[k];
