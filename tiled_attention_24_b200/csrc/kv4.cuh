@@ -259,8 +259,7 @@ constexpr int KV4_EVICT_CACHED = 16384;  // keys a CTA keeps; longer slices are 
 constexpr int KV4_EVICT_BINS = 2048;
 
 struct Kv4EvictShared {
-  int hist[KV4_EVICT_BINS];   // this CTA's
-  int total[KV4_EVICT_BINS];  // the cluster's, in its first CTA
+  int hist[2][KV4_EVICT_BINS];  // this CTA's, of one pass and the next; then the words' first list entries
   int2 warp[2][KV4_EVICT_WARPS];
   int2 cta[2][8];             // per CTA: equal keys; holes and sources
   uint32_t prefix;
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
       }
     }
   }
-  for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) sh.hist[i] = sh.total[i] = 0;
+  for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) sh.hist[0][i] = sh.hist[1][i] = 0;
   cluster.sync();
 
   // ---- 1. the threshold
@@ -327,56 +326,46 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     const uint32_t digits = d == 2 ? 1023u : 2047u;
+    int* hist = sh.hist[d & 1];
 #pragma unroll 4
     for (int i = tid; i < n; i += KV4_EVICT_THREADS) {
       const uint32_t key = key_at(i);
-      if ((key & mask) == prefix) atomicAdd(&sh.hist[(key >> shift) & digits], 1);
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & digits], 1);
+    }
+    cluster.sync();
+    if (d == 1)  // read by all before this pass's barrier, filled again in the next pass
+      for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) sh.hist[0][i] = 0;
+    // bins from the top, four to a thread: the one in which the need-th key lies
+    constexpr int PER = 4;
+    static_assert(PER * KV4_EVICT_THREADS == KV4_EVICT_BINS, "four bins a thread");
+    const int top = KV4_EVICT_BINS - PER * (tid + 1);
+    int c[PER] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int r = 0; r < CL; ++r) {
+      const int4 v = *reinterpret_cast<const int4*>(cluster.map_shared_rank(hist, r) + top);
+      c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
+    }
+    const int sum = c[0] + c[1] + c[2] + c[3];
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) sh.warp[0][warp].x = before;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) before += sh.warp[0][k].x;
+    before -= sum;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      if (before < need && need <= before + c[k]) {
+        sh.prefix = prefix | ((uint32_t)(top + PER - 1 - k) << shift);
+        sh.need = need - before;
+        sh.ties = c[k];
+      }
+      before += c[k];
     }
     __syncthreads();
-    int* total = cluster.map_shared_rank(sh.total, 0);
-    for (int i = tid; i < KV4_EVICT_BINS; i += KV4_EVICT_THREADS) {
-      const int c = sh.hist[i];
-      if (c) {
-        atomicAdd(&total[i], c);
-        sh.hist[i] = 0;
-      }
-    }
-    cluster.sync();
-    if (rank == 0) {
-      // bins from the top, four to a thread: the one in which the need-th key lies
-      constexpr int PER = KV4_EVICT_BINS / KV4_EVICT_THREADS;
-      int c[PER], sum = 0;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int bin = KV4_EVICT_BINS - 1 - (tid * PER + k);
-        c[k] = sh.total[bin];
-        sh.total[bin] = 0;
-        sum += c[k];
-      }
-      int before = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-      }
-      if (lane == 31) sh.warp[0][warp].x = before;
-      __syncthreads();
-      for (int k = 0; k < warp; ++k) before += sh.warp[0][k].x;
-      before -= sum;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        if (before < need && need <= before + c[k]) {
-          const uint32_t found = prefix | ((uint32_t)(KV4_EVICT_BINS - 1 - (tid * PER + k)) << shift);
-          for (int r = 0; r < CL; ++r) {
-            *cluster.map_shared_rank(&sh.prefix, r) = found;
-            *cluster.map_shared_rank(&sh.need, r) = need - before;
-            *cluster.map_shared_rank(&sh.ties, r) = c[k];
-          }
-        }
-        before += c[k];
-      }
-    }
-    cluster.sync();
     prefix = sh.prefix;
     need = sh.need;
     mask |= digits << shift;
@@ -445,9 +434,25 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
   for (int k = w0; k < w0 + words; ++k) count.x += __popc(hole_bits(k)), count.y += __popc(source_bits(k));
   int2 at = before_me(count, 1, all);
   const int moves = all.x;
-  for (int k = w0; k < w0 + words; ++k) {
-    for (unsigned m = hole_bits(k); m; m &= m - 1) hole_list[at.x++] = j0 + 32 * k + __ffs(m) - 1;
-    for (unsigned m = source_bits(k); m; m &= m - 1) source_list[at.y++] = j0 + 32 * k + __ffs(m) - 1;
+  if constexpr (CACHED) {  // a warp per word.  No source lies before the word in which n_keep falls
+    static_assert(KV4_EVICT_CACHED <= 32 * KV4_EVICT_THREADS, "a word a thread");
+    int* first = sh.hist[0];
+    if (tid < slice / 32) first[tid] = j0 + 32 * tid < p.n_keep ? at.x : at.y;
+    __syncthreads();
+    const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int k = warp; k < slice / 32; k += KV4_EVICT_WARPS) {
+      const unsigned holes = hole_bits(k), sources = source_bits(k);
+      const int slot = j0 + 32 * k + lane;
+      if ((holes >> lane) & 1u) hole_list[first[k] + __popc(holes & below)] = slot;
+      if ((sources >> lane) & 1u)
+        source_list[(j0 + 32 * k < p.n_keep ? 0 : first[k]) + __popc(sources & below)] = slot;
+    }
+  } else {
+    for (int k = w0; k < w0 + words; ++k) {
+      for (unsigned m = hole_bits(k); m; m &= m - 1) hole_list[at.x++] = j0 + 32 * k + __ffs(m) - 1;
+      for (unsigned m = source_bits(k); m; m &= m - 1) source_list[at.y++] = j0 + 32 * k + __ffs(m) - 1;
+    }
   }
   const int front = min(n, p.n_keep - j0);
   const bool copy = w_out != w || pos_out != pos;
@@ -472,17 +477,22 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
   cluster.sync();  // the lists are complete, and nobody reads weights or positions below n_keep any more
   constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 2;  // 16 bytes of codes a lane
   const int sub = lane % LANES;
-  for (int m0 = (rank * KV4_EVICT_WARPS + warp) * ROWS * DEEP; m0 < moves; m0 += CL * KV4_EVICT_WARPS * ROWS * DEEP) {
-    uint4 kc[DEEP], vc[DEEP];
-    T sc[DEEP];
-    uint32_t side[DEEP];
-    int to[DEEP], from[DEEP];
+  int to[DEEP], from[DEEP];
+  auto pairs = [&](int m0) {
 #pragma unroll
     for (int k = 0; k < DEEP; ++k) {
       const int m = m0 + k * ROWS + lane / LANES;
       to[k] = m < moves ? __ldcg(hole_list + m) : -1;
       from[k] = m < moves ? __ldcg(source_list + m) : 0;
     }
+  };
+  const int step = CL * KV4_EVICT_WARPS * ROWS * DEEP;
+  int m0 = (rank * KV4_EVICT_WARPS + warp) * ROWS * DEEP;
+  pairs(m0);
+  for (; m0 < moves; m0 += step) {
+    uint4 kc[DEEP], vc[DEEP];
+    T sc[DEEP];
+    uint32_t side[DEEP];
 #pragma unroll
     for (int k = 0; k < DEEP; ++k)
       if (to[k] >= 0) {
@@ -494,18 +504,22 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
           side[k] = sub ? (uint32_t)pos[from[k]] : __float_as_uint(w[from[k]]);
         }
       }
+    int dsts[DEEP], srcs[DEEP];
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) dsts[k] = to[k], srcs[k] = from[k];
+    pairs(m0 + step);  // the next rows' places, while these rows are on their way
 #pragma unroll
     for (int k = 0; k < DEEP; ++k)
-      if (to[k] >= 0) {
-        const size_t dst = row0 + to[k];
+      if (dsts[k] >= 0) {
+        const size_t dst = row0 + dsts[k];
         reinterpret_cast<uint4*>(p.kc + dst * (D / 2))[sub] = kc[k];
         reinterpret_cast<uint4*>(p.vc + dst * (D / 2))[sub] = vc[k];
         if (sub < 2) {
           *reinterpret_cast<T*>((sub ? p.vs : p.ks) + dst * NG) = sc[k];
           if (sub)
-            pos_out[to[k]] = (int)side[k];
+            pos_out[dsts[k]] = (int)side[k];
           else
-            w_out[to[k]] = __uint_as_float(side[k]), kept[to[k]] = from[k];
+            w_out[dsts[k]] = __uint_as_float(side[k]), kept[dsts[k]] = srcs[k];
         }
       }
   }
