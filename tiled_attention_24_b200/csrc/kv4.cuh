@@ -42,10 +42,6 @@ __device__ __forceinline__ uint32_t kv4_half(const uint2& w, int g) {
   return (g & 1) ? (v >> 16) : (v & 0xFFFFu);
 }
 __device__ __forceinline__ uint32_t kv4_half(const uint32_t& w, int g) { return (g & 1) ? (w >> 16) : (w & 0xFFFFu); }
-__device__ __forceinline__ uint2 kv4_join(const uint32_t (&h)[4]) {
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-}
-__device__ __forceinline__ uint32_t kv4_join(const uint32_t (&h)[2]) { return h[0] | (h[1] << 16); }
 // code i (0..3) of a halfword of four
 __device__ __forceinline__ float kv4_code(uint32_t h, int i) { return (float)((int)(h << (28 - 4 * i)) >> 28); }
 __device__ __forceinline__ float kv4_scale(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -65,34 +61,45 @@ struct Kv4AppendParams {
 
 // One K and one V row by the 8 lanes of their pieces (lane u: channels 4u..4u+3 of
 // each of the 2 NG groups).  What a group needs once is done once: amax by a
-// butterfly that halves the groups a lane holds at each step, on pairs of bf16 bit
-// patterns (ordered like the values, infinities and NaNs on top); the scale and its
-// reciprocal by one lane (two where d = 64), which hands the reciprocal round.
+// butterfly that halves the groups a lane holds at each step, on pairs of bf16 (a NaN
+// wins; the sign of a maximum means nothing); the scale and its reciprocal by one lane
+// (two where d = 64), which hands the reciprocal round.
 //
 // The codes need rne(x / s) exactly, without a divide per element: with
-// r = rn(1/s), fma(x, r, 6144) - 6144 is x r rounded to a multiple of 2^-11.
+// r = rn(1/s), t = fma(x, r, 6144) is 6144 + x r rounded to a multiple of 2^-11.
 // x and s have 8 significant bits, so a quotient of magnitude <= 7.6 is either
 // exactly k + 1/2 or at least 2^-2 / 255 > 9e-4 away from it, and x r is within
 // 5e-7 of the quotient: rounded to 2^-11 (at most 2.5e-4 away) the ties are
-// ties again and nothing else is one.  Adding and taking off 1.5 * 2^23 then rounds
-// to even.  |x / s| <= 7 (1 + 2^-8), so no code exceeds 7.  Four codes become a
-// halfword as the number sum 16^i (c_i + 8), whose digits are the nibbles with
-// their sign bits flipped.  Groups with an infinity or a NaN, and scales below
+// ties again and nothing else is one.  t - 6144 + 8 + 1.5 * 2^23, one addition, then
+// rounds to even and leaves c + 8 in the low bits of the number.  |x / s| <= 7 (1 +
+// 2^-8), so c + 8 is 1 to 15: four make a halfword by shifts and sums, a nibble each,
+// with the sign bits flipped.  Groups with an infinity or a NaN, and scales below
 // 2^-100, where 1/s may overflow or s has lost bits, are redone with the divide.
 //
-// Bound by HBM with this (4 x 16 heads x 4096 tokens, d = 128, 173 MB); a divide per
-// group and lane and integer packing took 14 instructions a value and 53 us.
-__device__ __forceinline__ uint32_t kv4_halfword(uint32_t lo, uint32_t hi, float r) {
-  const uint64_t rr = f2(r, r), six = f2(6144.f, 6144.f), nsix = f2(-6144.f, -6144.f);
-  const uint64_t big = f2(12582912.f, 12582912.f), nbig = f2(-12582912.f, -12582912.f);
-  uint64_t a = ffma2(f2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u)), rr, six);
-  uint64_t b = ffma2(f2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), rr, six);
-  a = fadd2(fadd2(fadd2(a, nsix), big), nbig);  // c0, c1
-  b = fadd2(fadd2(fadd2(b, nsix), big), nbig);  // c2, c3
-  float c0, c1;
-  f2_split(ffma2(b, f2(256.f, 256.f), a), c0, c1);                // c0 + 256 c2, c1 + 256 c3
-  const float n = fmaf(c1, 16.f, c0) + (8388608.f + 34952.f);     // + 0x8888, in the low bits
-  return (__float_as_uint(n) & 0xFFFFu) ^ 0x8888u;
+// 4 x 16 heads x 4096 tokens, d = 128 (173 MB, 27 us at the copy bandwidth): 31 us.
+// Maxima on unpacked halves and sums of c_i 16^i as floats took 36, a divide per group
+// and lane with integer packing 53: the ALU pipe bounded both.
+__device__ __forceinline__ uint32_t kv4_halfword(uint32_t lo, uint32_t hi, float r) {  // the bits above are not 0
+  const uint64_t rr = f2(r, r), six = f2(6144.f, 6144.f), big = f2(12576776.f, 12576776.f);
+  const uint64_t a = fadd2(ffma2(f2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u)), rr, six), big);
+  const uint64_t b = fadd2(ffma2(f2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), rr, six), big);
+  float c0, c1, c2, c3;
+  f2_split(a, c0, c1);
+  f2_split(b, c2, c3);
+  return __float_as_uint(c0) + (__float_as_uint(c1) << 4) + ((__float_as_uint(c2) + (__float_as_uint(c3) << 4)) << 8);
+}
+constexpr uint32_t KV4_FLIP = 0x88888888u;
+__device__ __forceinline__ uint2 kv4_join_flipped(const uint32_t (&h)[4]) {
+  return make_uint2(__byte_perm(h[0], h[1], 0x5410) ^ KV4_FLIP, __byte_perm(h[2], h[3], 0x5410) ^ KV4_FLIP);
+}
+__device__ __forceinline__ uint32_t kv4_join_flipped(const uint32_t (&h)[2]) {
+  return __byte_perm(h[0], h[1], 0x5410) ^ KV4_FLIP;
+}
+// per half: the larger magnitude, NaN if either is; the sign may be either's
+__device__ __forceinline__ uint32_t kv4_amax2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 __device__ __noinline__ uint32_t kv4_halfword_slow(uint32_t lo, uint32_t hi, uint32_t scale_bits) {
   const float s = kv4_scale(scale_bits);
@@ -127,13 +134,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
   uint32_t m[NG];  // amax of groups 2i (low half) and 2i + 1
 #pragma unroll
   for (int g = 0; g < 2 * NG; g += 2) {
-    uint32_t a[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t v = __vmaxu2(w[g + e].x & 0x7FFF7FFFu, w[g + e].y & 0x7FFF7FFFu);
-      a[e] = max(v & 0xFFFFu, v >> 16);
-    }
-    m[g / 2] = a[0] | (a[1] << 16);
+    const uint32_t a = kv4_amax2(w[g].x, w[g].y), c = kv4_amax2(w[g + 1].x, w[g + 1].y);
+    m[g / 2] = kv4_amax2(__byte_perm(a, c, 0x5410), __byte_perm(a, c, 0x7632));
   }
   // halve the pairs held at each step; then lane u has pair `pair`, groups 2 pair, 2 pair + 1
   int pair = 0, bit = 4;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t give = up ? m[e] : m[(e + 2) % NG], keep = up ? m[(e + 2) % NG] : m[e];
-      m[e] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+      m[e] = kv4_amax2(keep, __shfl_xor_sync(0xffffffffu, give, 4));
     }
     pair = up ? 2 : 0;
     bit = 2;
@@ -150,13 +152,13 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
   {
     const bool up = u & bit;
     const uint32_t give = up ? m[0] : m[1], keep = up ? m[1] : m[0];
-    m[0] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, bit));
+    m[0] = kv4_amax2(keep, __shfl_xor_sync(0xffffffffu, give, bit));
     pair += up ? 1 : 0;
   }
 #pragma unroll
-  for (int o = NG == 4 ? 1 : 2; o > 0; o >>= 1) m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+  for (int o = NG == 4 ? 1 : 2; o > 0; o >>= 1) m[0] = kv4_amax2(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
   const int mine = 2 * pair + (u & 1);  // this lane's group
-  const uint32_t top = (u & 1) ? m[0] >> 16 : m[0] & 0xFFFFu;
+  const uint32_t top = ((u & 1) ? m[0] >> 16 : m[0]) & 0x7FFFu;
   uint32_t bits = pack_bf16(__fdiv_rn(__uint_as_float(top << 16), 7.f), 0.f) & 0xFFFFu;
   if (top >= 0x7F80u) bits = 0x7FC0u;
   const float s = kv4_scale(bits);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
     for (int g = 0; g < 2 * NG; ++g) {
       const int from = NG == 4 ? ((g & 4) ? 4 : 0) | ((g & 2) ? 2 : 0) | (g & 1) : ((g & 2) ? 4 : 0) | (g & 1);
       const uint32_t sb = __shfl_sync(0xffffffffu, bits, base + from);
-      if (__shfl_sync(0xffffffffu, (int)odd, base + from)) h[g] = kv4_halfword_slow(w[g].x, w[g].y, sb);
+      if (__shfl_sync(0xffffffffu, (int)odd, base + from)) h[g] = kv4_halfword_slow(w[g].x, w[g].y, sb) ^ (KV4_FLIP & 0xFFFFu);
     }
   }
   if (!live) return;
@@ -184,8 +186,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4AppendParams p
   uint32_t hk[NG], hv[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) hk[g] = h[g], hv[g] = h[NG + g];
-  reinterpret_cast<T*>(p.kc + dst * (D / 2))[u] = kv4_join(hk);
-  reinterpret_cast<T*>(p.vc + dst * (D / 2))[u] = kv4_join(hv);
+  reinterpret_cast<T*>(p.kc + dst * (D / 2))[u] = kv4_join_flipped(hk);
+  reinterpret_cast<T*>(p.vc + dst * (D / 2))[u] = kv4_join_flipped(hv);
   // every group's scale by the lane that made it (d = 64: by the first of the two)
   if (NG == 4 || !(u & 2)) (mine < NG ? p.ks : p.vs)[dst * NG + mine % NG] = (uint16_t)bits;
   if (u == 2 && p.weights) p.weights[dst] = 0.f;
