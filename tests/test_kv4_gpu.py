@@ -245,6 +245,23 @@ def test_decode_scales_of_any_size(cuda_lib, d, mag):
     check_decode(got, ref, d, f"mag {mag}")
 
 
+# 8 partials a row and fewer, up to 64, more: each merged in its own way; 20 heads to a
+# cache head are weighed in three turns, the last of four
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,cap,lens,splits", [
+    (40, 2, 1104, [1101, 0, 64], 8), (40, 2, 1104, [1, 1090, 700], 9), (8, 2, 4112, [4100, 0, 2077], 63),
+    (20, 1, 4400, [4399, 1500, 3], 64), (6, 1, 9008, [9001, 5, 0], 140),
+])
+def test_decode_merges(cuda_lib, Hq, Hkv, cap, lens, splits, d):
+    B = len(lens)
+    host, dev = make_cache(B, Hkv, cap, d, 31 + splits)
+    g = torch.Generator().manual_seed(splits)
+    q = torch.randn(B, Hq, 1, d, generator=g).bfloat16()
+    w0 = torch.rand(B, Hkv, cap, generator=g).cuda()
+    got = run_decode(cuda_lib, q.cuda(), dev, ints(lens), d ** -0.5, splits, w0)
+    check_decode(got, O.decode(q, host["kc"], host["ks"], host["vc"], host["vs"], lens, d ** -0.5), d, f"merge {splits}", w0)
+
+
 def test_decode_many_sequences(cuda_lib):
     """More sequences than a warp has lanes, most of them empty or tiny, one long."""
     B, Hq, Hkv, cap, d = 77, 4, 2, 1008, 64
