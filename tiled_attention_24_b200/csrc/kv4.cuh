@@ -249,13 +249,19 @@ __device__ __forceinline__ uint32_t kv4_rank_key(float w, int pos, long long fir
 // The whole eviction of one (batch, cache head) by one cluster of up to 8 CTAs,
 // each with a contiguous slice of the slots, keys kept in shared memory:
 //   1. the n_keep-th largest key, 11 + 11 + 10 bits at a time: histograms per CTA,
-//      added up in the first CTA's shared memory, which finds the digit;
+//      which every CTA adds up, so that each finds the digit;
 //   2. keys above it stay, and as many equal ones as are wanted, lowest slots first
 //      (ranks by ballots, prefix sums over warps and CTAs);
 //   3. the lists of holes (below n_keep, not kept) and sources (kept, at or beyond
 //      n_keep), both in slot order, and the r-th source moves into the r-th hole.
 // Rows move from slots >= n_keep into slots < n_keep only, so no row is read after
 // it was overwritten and a repeated call moves the same rows again.
+// 16 sequences of up to 32768 slots to 16384, 8 cache heads, d = 128 (138 MB, 21 us at
+// the copy bandwidth): 60 us.  About 25 are a chain of barriers over a few slots a
+// thread (load 5, each digit 3, places 2, lists 3), 25 the moves: rows of 64 + 8 + 8
+// bytes picked out of sectors of 32 and written back, near the bandwidth.  Two CTAs of
+// 512 threads on an SM: 3 spill (68 us), clusters of 2 or 8 leave SMs idle or wait for
+// room (92, 97); two rows a lane in flight gain nothing (60).
 constexpr int KV4_EVICT_THREADS = 512, KV4_EVICT_WARPS = KV4_EVICT_THREADS / 32;
 constexpr int KV4_EVICT_CACHED = 16384;  // keys a CTA keeps; longer slices are ranked from memory each time
 constexpr int KV4_EVICT_BINS = 2048;
@@ -288,9 +294,22 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
   float* w_out = p.weights_out + row0;
   int* pos_out = p.positions_out + row0;
   if (L <= p.n_keep) {  // nothing to evict
-    for (int j = rank * KV4_EVICT_THREADS + tid; j < p.n_keep; j += CL * KV4_EVICT_THREADS) {
-      kept[j] = j < L ? j : -1;
-      if (j < L) w_out[j] = w[j], pos_out[j] = pos[j];
+    const int step = CL * KV4_EVICT_THREADS;
+    for (int j0 = rank * KV4_EVICT_THREADS + tid; j0 < p.n_keep; j0 += 8 * step) {  // 8 slots a thread in flight
+      float a[8];
+      int c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * step;
+        a[k] = j < L ? w[j] : 0.f;
+        c[k] = j < L ? pos[j] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * step;
+        if (j < p.n_keep) kept[j] = j < L ? j : -1;
+        if (j < L) w_out[j] = a[k], pos_out[j] = c[k];
+      }
     }
     return;
   }
@@ -302,6 +321,10 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
   auto key_at = [&](int i) -> uint32_t {
     return CACHED ? keys[i] : kv4_rank_key(w[j0 + i], pos[j0 + i], first_recent);
   };
+  // Slots below n_keep that stay keep their places; copied before it is known which
+  // stay, since every other of them is a hole that a row is moved into later
+  const int front = min(n, p.n_keep - j0);
+  const bool copy = w_out != w || pos_out != pos;
   if (CACHED) {  // 8 slots a thread in flight
     for (int i = tid; i < n; i += 8 * KV4_EVICT_THREADS) {
       float a[8];
@@ -316,6 +339,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
       for (int k = 0; k < 8; ++k) {
         const int at = i + k * KV4_EVICT_THREADS;
         if (at < n) keys[at] = kv4_rank_key(a[k], c[k], first_recent);
+        if (copy && at < front) w_out[j0 + at] = a[k], pos_out[j0 + at] = c[k];
       }
     }
   }
@@ -356,7 +380,11 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
     }
     if (lane == 31) sh.warp[0][warp].x = before;
     __syncthreads();
-    for (int k = 0; k < warp; ++k) before += sh.warp[0][k].x;
+#pragma unroll
+    for (int k = 0; k < KV4_EVICT_WARPS; ++k) {
+      const int v = sh.warp[0][k].x;
+      if (k < warp) before += v;
+    }
     before -= sum;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -371,6 +399,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
     prefix = sh.prefix;
     need = sh.need;
     mask |= digits << shift;
+    if (sh.ties == need) break;  // all keys of this digit stay, whatever their lower ones: no key is below the prefix
   }
 
   // ---- 2. who stays: a bit for each slot
@@ -386,6 +415,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
     if (lane == 31) sh.warp[which][warp] = up;
     __syncthreads();
     int2 before = make_int2(up.x - c.x, up.y - c.y), mine = make_int2(0, 0);
+#pragma unroll
     for (int k = 0; k < KV4_EVICT_WARPS; ++k) {
       const int2 v = sh.warp[which][k];
       if (k < warp) before.x += v.x, before.y += v.y;
@@ -446,6 +476,7 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
     for (int k = warp; k < slice / 32; k += KV4_EVICT_WARPS) {
       const unsigned holes = hole_bits(k), sources = source_bits(k);
       const int slot = j0 + 32 * k + lane;
+      if (32 * k + lane < front && ((keep_bits[k] >> lane) & 1u)) kept[slot] = slot;
       if ((holes >> lane) & 1u) hole_list[first[k] + __popc(holes & below)] = slot;
       if ((sources >> lane) & 1u)
         source_list[(j0 + 32 * k < p.n_keep ? 0 : first[k]) + __popc(sources & below)] = slot;
@@ -455,29 +486,15 @@ __global__ void __launch_bounds__(KV4_EVICT_THREADS, 2) kv4_evict_kernel(const K
       for (unsigned m = hole_bits(k); m; m &= m - 1) hole_list[at.x++] = j0 + 32 * k + __ffs(m) - 1;
       for (unsigned m = source_bits(k); m; m &= m - 1) source_list[at.y++] = j0 + 32 * k + __ffs(m) - 1;
     }
-  }
-  const int front = min(n, p.n_keep - j0);
-  const bool copy = w_out != w || pos_out != pos;
-  for (int i = tid; i < front; i += 8 * KV4_EVICT_THREADS) {  // 8 slots a thread in flight
-    float a[8];
-    int c[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = i + k * KV4_EVICT_THREADS;
-      a[k] = copy && s < front ? w[j0 + s] : 0.f;
-      c[k] = copy && s < front ? pos[j0 + s] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = i + k * KV4_EVICT_THREADS;
-      if (s < front && ((keep_bits[s / 32] >> lane) & 1u)) {
-        kept[j0 + s] = j0 + s;
-        if (copy) w_out[j0 + s] = a[k], pos_out[j0 + s] = c[k];
+    for (int i = tid; i < front; i += KV4_EVICT_THREADS)
+      if ((keep_bits[i / 32] >> lane) & 1u) {
+        const int slot = j0 + i;
+        kept[slot] = slot;
+        if (copy) w_out[slot] = w[slot], pos_out[slot] = pos[slot];
       }
-    }
   }
   cluster.sync();  // the lists are complete, and nobody reads weights or positions below n_keep any more
-  constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 2;  // 16 bytes of codes a lane
+  constexpr int LANES = D / 32, ROWS = 32 / LANES, DEEP = 1;  // 16 bytes of codes a lane
   const int sub = lane % LANES;
   int to[DEEP], from[DEEP];
   auto pairs = [&](int m0) {
