@@ -259,7 +259,7 @@ __device__ __forceinline__ uint32_t kv4_rank_key(float w, int pos, long long fir
 // 16 sequences of up to 32768 slots to 16384, 8 cache heads, d = 128 (138 MB, 21 us at
 // the copy bandwidth): 60 us.  About 25 are a chain of barriers over a few slots a
 // thread (load 5, each digit 3, places 2, lists 3), 25 the moves: rows of 64 + 8 + 8
-// bytes picked out of sectors of 32 and written back, near the bandwidth.  Two CTAs of
+// bytes picked out of sectors of 32 and written back.  Two CTAs of
 // 512 threads on an SM: 3 spill (68 us), clusters of 2 or 8 leave SMs idle or wait for
 // room (92, 97); two rows a lane in flight gain nothing (60).
 constexpr int KV4_EVICT_THREADS = 512, KV4_EVICT_WARPS = KV4_EVICT_THREADS / 32;
