@@ -18,6 +18,9 @@
 //   warp 8          TMA producer; per query row -lse log2(e) and the last key it
 //                   sees, and what the other roles need to know of a step
 //   warp 9          MMA issuer, tensor-memory owner
+// Bound by the exponentials, one a score (MUFU 61 % busy; 64 us of them alone), and the
+// hand-over of tiles: 4096 causal queries, 32 / 8 heads, d = 128: 110 us; the last 32
+// queries of 4 x 16384 keys: 41 us, K at 3.4 TB/s.
 #pragma once
 #include <type_traits>
 
