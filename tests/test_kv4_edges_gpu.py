@@ -1,0 +1,115 @@
+"""GPU parity of the 4-bit cache's decode where values are of very different sizes,
+against an fp64 computation of the definition.
+
+Tolerances, from the arithmetic (p: probability, s: scale of v's group, n: slots):
+
+* scores: fp32 sums of d exact products and the factors of scale: off by at most
+  ex = (d + 16) 2^-23 max_j sum_c |q_c k_c| scale; a probability by a factor within
+  ep = 2 ex + 2^-21 + n 2^-24 (numerator and denominator; two exponentials of 2^-22;
+  the sum, at most n / 8 serial additions of 2^-24 each in a lane, and one of a few
+  partials);
+* o: p s is rounded to fp16 once, 2^-11 (half of its eps).  Below fp16's normal numbers,
+  2^-14, it is off by 2^-25 instead or lost whole: with s taken so that the largest scale
+  s' is at most 2^15 and at least 2^14, and a sum of p no smaller than 2^-8, that is
+  2^(-25 - 14 + 8) s' = 2^-31 s' for slots with p s < 2^(-14 - 14 + 8) s' = 2^-20 s', times a
+  code of at most 8: min(8 p s, 2^-28 s') each;
+* the offset of the codes: two matrix instructions a step of 16 slots, each a sum of 17
+  addends cut at 2^-24 of the largest: 2 * 17 * 15 * 2^-24 < 2^-15 of p s, and 2^-24 of
+  what has been summed up so far for 16 addends twice a step: n 2^-23 of sum p |v|;
+* the result in bf16: 2^-8 of itself (half of its eps);
+* lse: ep + 2^-22 |lse|; weights: w ep + 2^-23 of the sum they join, per head.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as O
+from tests.test_kv4_gpu import ints, make_cache, run_decode, to_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(q, host, lens, scale):
+    """o, lse, w and the two parts of o's bound, fp64, from the definition."""
+    q = q.double().numpy()
+    B, Hq, _, d = q.shape
+    Hkv, cap = host["kc"].shape[1:3]
+    G = Hq // Hkv
+    o, lse, w = np.zeros((B, Hq, d)), np.full((B, Hq), -np.inf), np.zeros((B, Hkv, cap))
+    grid, pv, ex = np.zeros((B, Hq, d)), np.zeros((B, Hq, d)), np.zeros((B, Hq))
+    for b, n in enumerate(lens):
+        for h in range(Hkv if n else 0):
+            k, v = (O.values(host[c][b, h, :n], host[s][b, h, :n]) for c, s in (("kc", "ks"), ("vc", "vs")))
+            s = np.repeat(host["vs"][b, h, :n].astype(np.float64), 32, axis=-1)
+            top = s.max(axis=0)
+            for a in range(h * G, (h + 1) * G):
+                x = k @ q[b, a, 0] * scale
+                z = x.max() + np.log(np.exp(x - x.max()).sum())
+                p = np.exp(x - z)
+                o[b, a], lse[b, a] = p @ v, z
+                w[b, h, :n] += p
+                ps = p[:, None] * s
+                pv[b, a] = p @ np.abs(v)
+                grid[b, a] = 2.0 ** -15 * ps.sum(axis=0) + np.where(ps < 2.0 ** -20 * top, np.minimum(8 * ps, 2.0 ** -28 * top), 0).sum(axis=0)
+                ex[b, a] = (d + 16) * 2.0 ** -23 * (np.abs(k) @ np.abs(q[b, a, 0])).max() * scale
+    return o, lse, w, pv, grid, ex
+
+
+def check(got, ref, lens, what, w0=None):
+    o, lse, w = (None if t is None else t.double().cpu().numpy() for t in got)
+    ro, rl, rw, pv, grid, ex = ref
+    n = np.array(lens, dtype=np.float64)[:, None]
+    ep = 2 * ex + 2.0 ** -21 + n * 2.0 ** -24
+    tol = (2.0 ** -11 + ep + n * 2.0 ** -23)[..., None] * pv + grid + 2.0 ** -8 * np.abs(ro) + 2.0 ** -133
+    for name, err in (("lse", np.abs(lse[..., 0] - rl) - ep - 2.0 ** -22 * np.abs(rl)), ("o", np.abs(o[:, :, 0] - ro) - tol)):
+        assert np.isfinite(err).all() and (err <= 0).all(), f"{what}: {name} off by {err.max()} beyond its bound"
+    if w is not None:
+        w0 = w0.double().cpu().numpy()
+        G = ex.shape[1] // w0.shape[1]
+        err = np.abs(w - w0 - rw) - (rw * ep.reshape(*w0.shape[:2], G).max(axis=2)[..., None] + G * 2.0 ** -23 * np.abs(w0 + rw))
+        assert np.isfinite(err).all() and (err <= 0).all(), f"{what}: weights off by {err.max()} beyond their bound"
+
+
+def upload(host):
+    return {n: (torch.from_numpy(v) if v.dtype == np.uint8 else to_bf16(v)).cuda() for n, v in host.items()}
+
+
+def case(Hkv, cap, d, seed):
+    host, _ = make_cache(1, Hkv, cap, d, seed)
+    return {n: v.astype(np.float32) if v.dtype != np.uint8 else v for n, v in host.items()}
+
+
+def both(ta, q, host, lens, scale, what, splits=(1, 0)):
+    dev, ref = upload(host), reference(q, host, lens, scale)
+    w0 = torch.zeros(host["kc"].shape[:3], device="cuda")
+    for s in splits:
+        check(run_decode(ta, q.cuda(), dev, ints(lens), scale, s, w0), ref, lens, f"{what}, {s} splits", w0)
+
+
+# ------------------------------------------------------------------ values of very different sizes
+@pytest.mark.parametrize("Hq,d", [(3, 64), (4, 128), (6, 128), (8, 64)])
+def test_zero_values_of_many_slots(cuda_lib, Hq, d):
+    """V all zero: the sums of probabilities know nothing of V's size.  20000 slots whose
+    scores lie just under 8 (log2 units) above the first tile's."""
+    n = 20000
+    host = case(1, n, d, 1)
+    host["vs"][:], host["ks"][:] = 0, 0
+    host["ks"][:, :, 64:] = 1
+    k = np.zeros((1, 1, n, d))
+    k[..., 64:, 5] = 7
+    host["kc"] = O.pack(k.astype(np.int8))
+    q = torch.zeros(1, Hq, 1, d)
+    q[0, :, 0, 5] = 1.0 - torch.arange(Hq) / 16          # exact in bf16
+    both(cuda_lib, q.bfloat16(), host, [n], 7.8 / 7 * np.log(2.0), "zero values")
+
+
+@pytest.mark.parametrize("Hq,d", [(2, 128), (4, 64), (7, 64), (16, 128)])
+@pytest.mark.parametrize("first,then", [(0.0, 2.0 ** 30), (2.0 ** 30, 0.0), (2.0 ** -110, 2.0 ** 60), (2.0 ** 100, 2.0 ** -60)])
+@pytest.mark.parametrize("at", [64, 130, 300])
+def test_values_grow_or_shrink_along_the_row(cuda_lib, Hq, d, first, then, at):
+    """A slot's probability does not depend on what its or another's value is."""
+    host = case(1, 400, d, 2)
+    host["vs"][:, :, :at] *= np.float32(first)
+    host["vs"][:, :, at:] *= np.float32(then)
+    q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(at)).bfloat16()
+    both(cuda_lib, q, host, [391], d ** -0.5, f"values {first} then {then}", splits=(1, 0, 3))

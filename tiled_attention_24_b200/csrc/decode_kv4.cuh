@@ -10,8 +10,8 @@
 // (batch by batch, cache head by cache head), cut into equal pieces, one per
 // warp: however lengths are spread, every warp streams the same number of bytes.
 // A piece may begin and end inside a row; each (row, piece) leaves a partial
-// output, its sum and the exponent both are relative to, and a second kernel
-// merges a row's partials.  A weight needs the log-sum-exp of the whole row, so
+// output, its sum of probabilities and the exponent that is relative to, and a second
+// kernel merges a row's partials.  A weight needs the log-sum-exp of the whole row, so
 // the first kernel leaves the scores x in the workspace, fp32 (8 bytes a slot and
 // head written and read, mostly in L2, against 4.5 bits a channel to read K
 // again), and the second one turns them into weights.
@@ -33,8 +33,8 @@ struct DecKv4Params {
   const uint16_t* q;             // [B][Hq][D] bf16
   const uint8_t *kc, *vc;        // [B][Hkv][cap][D/2]
   const uint16_t *ks, *vs;       // [B][Hkv][cap][D/32] bf16
-  float* o_part;                 // [partial][head of the block][D]
-  float2* ml_part;               // [partial][head of the block]: exponent, sum
+  float* o_part;                 // [partial][head of the block][D], over the partial's sum
+  float2* ml_part;               // [partial][head of the block]: exponent M, sum l of 2^(x - M)
   float* x;                      // [B*Hq][cap] scores, or null
   const int* seqlens;            // [B]
   int B, Hkv, group, cap;
@@ -53,6 +53,9 @@ struct DecKv4Params {
 // slots at a time 169 to 178).
 constexpr int KV4_TILE = 64;                // slots of a tile
 constexpr int KV4_WARPS = 4, KV4_CTAS = 2;  // warps of a CTA, CTAs of an SM
+// bf16x2 words of exponents: the least reference of V's scales, 2^-112 (2^15 over it
+// is the largest power of two), and what a reference is taken from to give that quotient
+constexpr uint32_t KV4_VREF0 = ((127 - 112) << 7) * 0x10001u, KV4_VUP = ((2 * 127 + 15) << 7) * 0x10001u;
 
 template <int NG>
 struct DecKv4Cfg {
@@ -64,7 +67,8 @@ struct DecKv4Cfg {
   static constexpr int BAR_OFF = WARPS * STAGES * STAGE;
   static constexpr int SMEM = BAR_OFF + WARPS * STAGES * 8 + WARPS * 4;
   // lazy rescale: the reference max moves when a score exceeds it by TAU (log2
-  // units); probabilities are taken 2^-TAU smaller, so that none exceeds 1
+  // units); probabilities are taken 2^-TAU smaller, so that none exceeds 1 and a
+  // piece's sum of them is from 2^-TAU to its number of slots, whatever the values
   static constexpr float TAU = 8.f;
 };
 
@@ -108,6 +112,11 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t flip) {
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "n"(MASK), "r"(flip));
   return d;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -129,6 +138,12 @@ __device__ __forceinline__ float kv4_half_float(uint32_t w, uint32_t pick) {
 __device__ __forceinline__ uint32_t kv4_word(const uint2& w, int i) { return i ? w.y : w.x; }
 __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w; }
 
+// the words of a row's scales times powers of two, exact as long as the product is normal
+__device__ __forceinline__ void kv4_scale_words(uint2& w, uint32_t up) { w.x = mul_bf16x2(w.x, up), w.y = mul_bf16x2(w.y, up); }
+__device__ __forceinline__ void kv4_scale_words(uint32_t& w, uint32_t up) { w = mul_bf16x2(w, up); }
+// 2^n as a float, 0 below the normal numbers; n <= 127
+__device__ __forceinline__ float kv4_exp2i(int n) { return n < -126 ? 0.f : __uint_as_float((uint32_t)(127 + n) << 23); }
+
 // Each warp is on its own: it walks its piece tile by tile through its own ring
 // of bulk copies, which runs ahead across the rows of the piece, and keeps its
 // own running max, sum and output.  r = lane / 4, t = lane % 4 below.
@@ -145,10 +160,11 @@ __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w;
 //     nibbles' channels carry 1/16.  The accumulators start from -8 sum q, which
 //     takes the offset out again, and each group's sum is scaled in fp32.
 //   O^T = V^T P^T, rows = channels, columns = heads: B is p times the slot's scale
-//     of the group, rounded to fp16 (the one rounding of P, 2^-11), with p
-//     taken times a power of two that keeps p s below 2^15.  That power follows
+//     of the group, rounded to fp16 (the one rounding of P, 2^-11), with the
+//     scale taken times a power of two that keeps p s below 2^15.  That power follows
 //     the largest scale met so far as the running max follows the scores, so
-//     a product counts from 2^-31 of the largest on.  The offset goes out 16
+//     a product counts from 2^-32 of the largest scale on; it never touches p or the
+//     sum of p, which know nothing of the values.  The offset goes out 16
 //     slots at a time through a second product with the constant -8: summed up over
 //     a long row it would swamp the result.  What the cancellation leaves is below
 //     2^-15 of p times the scale (a step of the grid), far inside the format's own
@@ -333,10 +349,10 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   // per head 2t, 2t + 1: reference max of y (scores before fx), threshold above which
-  // it moves, exponent M that probabilities are taken against; vref = 2^ev, bf16x2
+  // it moves, exponent M that probabilities are taken against.  vref: 2^ev, bf16x2, no
+  // scale so far is larger; vup: 2^(15 - ev)
   float my[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY}, M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
-  int ev = -100;
-  uint32_t vref = (uint32_t)((127 - 100) << 7) * 0x10001u;
+  uint32_t vref = KV4_VREF0, vup = KV4_VUP - KV4_VREF0;
   const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
   const uint32_t pick = hi ? 0x3244u : 0x1044u;  // PAIR: this lane's half of a word of scales, as a float
 
@@ -464,28 +480,37 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     if (__any_sync(0xffffffffu, h0 > thr[0] || h1 > thr[1] || vm != vref)) {
       uint32_t v = max(vm & 0xFFFFu, vm >> 16);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-      const int ev_new = v > (vref & 0xFFFFu) ? (int)(v >> 7) - 126 : ev;
+      for (int o = 4; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+      float fv = 1.f;  // what the outputs so far shrink by for V's sake
+      if (v > (vref & 0xFFFFu)) {
+        const uint32_t up = ((v & 0x7F80u) + 0x80u) * 0x10001u;
+        fv = kv4_exp2i(((int)(vref & 0xFFFFu) - (int)(up & 0xFFFFu)) >> 7);
+        vref = up, vup = KV4_VUP - up;
+      }
       float mx[2] = {h0, h1};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
         if (!(mx[k] > my[k])) mx[k] = my[k];
+        float f = 1.f;
         if (mx[k] != -INFINITY) {
-          const float Mn = fmaf(mx[k], fx[k], C::TAU + (float)(ev_new - 15));
-          const float f = my[k] == -INFINITY ? 0.f : ex2(M[k] - Mn);  // l and acc are 0 or NaN while my = -inf
+          const float Mn = fmaf(mx[k], fx[k], C::TAU);
+          f = my[k] == -INFINITY ? 0.f : ex2(M[k] - Mn);  // l and acc are 0 or NaN while my = -inf
           l[k] *= f;
-#pragma unroll
-          for (int n = 0; n < 2 * NG; ++n) acc[n][k] *= f, acc[n][k + 2] *= f;
           my[k] = mx[k];
           M[k] = Mn;
           thr[k] = mx[k] + C::TAU / fx[k];
         }
+        f *= fv;
+#pragma unroll
+        for (int n = 0; n < 2 * NG; ++n) acc[n][k] *= f, acc[n][k + 2] *= f;
       }
-      ev = ev_new;
-      vref = (uint32_t)((127 + ev) << 7) * 0x10001u;
     }
+#pragma unroll
+    for (int u = 0; u < C::U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) kv4_scale_words(vs[u][h], vup);
     float pr[C::U][4];
 #pragma unroll
     for (int u = 0; u < C::U; ++u) {
@@ -560,6 +585,13 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
   const size_t part = (size_t)(piece + at.item) * p.per_block;  // unique: the next piece or item has the next number
+  // A partial output is divided by its own sum: a mean of values, which no number of
+  // slots carries out of range.  2^(24 + ev - 15) over the sum, in three factors
+  float inv[2];
+  const int ev = (int)(vref >> 23) - 127, ev0 = ev / 2;
+  const float back0 = kv4_exp2i(ev0), back1 = kv4_exp2i(ev - ev0);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) inv[k] = l[k] == 0.f ? 0.f : 0x1p9f / l[k];
   if constexpr (PAIR) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -571,7 +603,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         float v[4];
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4)  // odd nibbles carry 16
-          v[i4] = (hi ? acc[4 * g + i4][k + 2] : acc[4 * g + i4][k]) * ((i4 & 1) ? 0x1p20f : 0x1p24f);
+          v[i4] = (hi ? acc[4 * g + i4][k + 2] : acc[4 * g + i4][k]) * ((i4 & 1) ? inv[k] * 0.0625f : inv[k]) * back0 * back1;
         *reinterpret_cast<float4*>(o + 64 * g) = make_float4(v[0], v[1], v[2], v[3]);
       }
       if (r == 0 && !hi) p.ml_part[part + h] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
@@ -582,9 +614,12 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     if (2 * t + k >= heads) continue;
     float* o = p.o_part + (part + 2 * t + k) * D + 4 * r;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)  // odd nibbles carry 16
-      *reinterpret_cast<float4*>(o + 32 * g) = make_float4(acc[2 * g][k] * 0x1p24f, acc[2 * g][k + 2] * 0x1p20f,
-                                                           acc[2 * g + 1][k] * 0x1p24f, acc[2 * g + 1][k + 2] * 0x1p20f);
+    for (int g = 0; g < NG; ++g) {  // odd nibbles carry 16
+      const float even = inv[k], odd = inv[k] * 0.0625f;
+      *reinterpret_cast<float4*>(o + 32 * g) =
+          make_float4(acc[2 * g][k] * even * back0 * back1, acc[2 * g][k + 2] * odd * back0 * back1,
+                      acc[2 * g + 1][k] * even * back0 * back1, acc[2 * g + 1][k + 2] * odd * back0 * back1);
+    }
     if (r == 0) p.ml_part[part + 2 * t + k] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
   }
   if (i == mine) break;
@@ -619,25 +654,31 @@ __device__ __forceinline__ float kv4_warp_max(float v) {
   for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
   return v;
 }
-// max M + log2 sum_c 2^(M_c - max M) l_c over a row's partials; whole warp
-__device__ __forceinline__ float kv4_row_lse2(const DecKv4Params& p, const Kv4Parts& parts) {
+// max M and sum_c 2^(M_c - max M) l_c over a row's partials; whole warp
+__device__ __forceinline__ float2 kv4_row_sum(const DecKv4Params& p, const Kv4Parts& parts) {
   const float2* ml = p.ml_part + parts.first;
   float m = -INFINITY, l = 0.f;
-  for (int c = threadIdx.x & 31; c < parts.n; c += 32) {
-    const float2 v = ml[(size_t)c * p.per_block];
-    const float grown = fmaxf(m, v.x);
-    l = fmaf(l, kv4_part_factor(m, grown), kv4_part_factor(v.x, grown) * v.y);
+#pragma unroll 1
+  for (int c = threadIdx.x & 31; c < parts.n; c += 128) {  // four in flight
+    float2 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = c + 32 * k < parts.n ? ml[(size_t)(c + 32 * k) * p.per_block] : make_float2(-INFINITY, 0.f);
+    const float grown = fmaxf(fmaxf(m, fmax3(v[0].x, v[1].x, v[2].x)), v[3].x);
+    l *= kv4_part_factor(m, grown);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l = fmaf(kv4_part_factor(v[k].x, grown), v[k].y, l);
     m = grown;
   }
   const float mx = kv4_warp_max(m);
   l *= kv4_part_factor(m, mx);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  return kv4_lse2(mx, l);
+  return make_float2(mx, l);
 }
 
 // What the pieces left becomes the outputs, in one launch.  The first CTAs merge: with
-// f = 2^(M_c - max M), O = sum f O_c / sum f l_c, LSE = ln 2 (max M + log2 sum f l_c);
+// f = 2^(M_c - max M), L = sum f l_c, O = sum (f l_c / L) O_c, LSE = ln 2 (max M + log2 L);
 // a row without slots has no partial, a NaN in a live slot stays one.  CTAS = 0: a
 // warp per row, its partials in loads of 8; 1: a CTA per row, a warp (half a warp of
 // d = 64) per partial; more: a CTA per 32 channels of a row, 32 partials at a time.
@@ -684,8 +725,8 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
           if (h0 + warp < p.group) parts = kv4_row_parts(p, bhk * p.group + h0 + warp);
         }
         if (h0 + warp < p.group) {
-          const float l2 = kv4_row_lse2(p, parts);
-          if (lane == 0) s_lse2[warp] = l2;
+          const float2 sum2 = kv4_row_sum(p, parts);
+          if (lane == 0) s_lse2[warp] = kv4_lse2(sum2.x, sum2.y);
         }
         __syncthreads();
       }
@@ -730,7 +771,8 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
   const float4* op = reinterpret_cast<const float4*>(p.o_part + parts.first * D) + first + lane4;
   const int o_step = p.per_block * (D / 4);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f, mx = -INFINITY;
+  float2 all = make_float2(0.f, 0.f);
+  float inv = 0.f;
   for (int c0 = 0; c0 < parts.n; c0 += BATCH * GROUPS) {
     float2 v[BATCH];
     float4 w[BATCH];
@@ -740,14 +782,13 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
       if (c < parts.n) v[k] = ml[(size_t)c * p.per_block], w[k] = op[(size_t)c * o_step];
     }
     if (c0 == 0) {
-      for (int c = lane; c < parts.n; c += 32) mx = fmaxf(mx, ml[(size_t)c * p.per_block].x);
-      mx = kv4_warp_max(mx);
+      all = kv4_row_sum(p, parts);
+      inv = 1.f / all.y;
     }
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       if (c0 + k * GROUPS + grp >= parts.n) break;
-      const float f = kv4_part_factor(v[k].x, mx);
-      l = fmaf(f, v[k].y, l);
+      const float f = kv4_part_factor(v[k].x, all.x) * v[k].y * inv;  // at most 1
       a.x = fmaf(f, w[k].x, a.x), a.y = fmaf(f, w[k].y, a.y), a.z = fmaf(f, w[k].z, a.z), a.w = fmaf(f, w[k].w, a.w);
     }
   }
@@ -755,29 +796,23 @@ __global__ void __launch_bounds__(KV4_FINISH_THREADS)
   for (int k = LANES; k < 32; k <<= 1) {
     a.x += __shfl_xor_sync(0xffffffffu, a.x, k), a.y += __shfl_xor_sync(0xffffffffu, a.y, k);
     a.z += __shfl_xor_sync(0xffffffffu, a.z, k), a.w += __shfl_xor_sync(0xffffffffu, a.w, k);
-    l += __shfl_xor_sync(0xffffffffu, l, k);
   }
   if (CTAS) {
     __shared__ float4 s_o[KV4_FINISH_WARPS][LANES];
-    __shared__ float s_l[KV4_FINISH_WARPS];
     if (lane < LANES) s_o[warp][lane] = a;
-    if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (tid >= LANES) return;
     a = make_float4(0.f, 0.f, 0.f, 0.f);
-    l = 0.f;
 #pragma unroll
     for (int k = 0; k < KV4_FINISH_WARPS; ++k) {
       const float4 w = s_o[k][tid];
       a.x += w.x, a.y += w.y, a.z += w.z, a.w += w.w;
-      l += s_l[k];
     }
   } else if (grp != 0) {
     return;
   }
-  const float inv = 1.f / l;
-  *out = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-  if (first + lane4 == 0) lse[row] = kv4_lse2(mx, l) * 0.69314718055994531f;
+  *out = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+  if (first + lane4 == 0) lse[row] = kv4_lse2(all.x, all.y) * 0.69314718055994531f;
 }
 
 }  // namespace ta
