@@ -113,3 +113,16 @@ def test_values_grow_or_shrink_along_the_row(cuda_lib, Hq, d, first, then, at):
     host["vs"][:, :, at:] *= np.float32(then)
     q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(at)).bfloat16()
     both(cuda_lib, q, host, [391], d ** -0.5, f"values {first} then {then}", splits=(1, 0, 3))
+
+
+@pytest.mark.parametrize("Hq,d", [(1, 128), (4, 64), (4, 128), (5, 64), (8, 128)])
+@pytest.mark.parametrize("spread", [2.0 ** 20, 2.0 ** 45])
+def test_groups_of_very_different_size(cuda_lib, Hq, d, spread):
+    """A channel group's values keep their accuracy beside much larger ones of another, which
+    stand before it in one cache head and behind it in the other."""
+    host = case(2, 400, d, 3)
+    size = spread ** np.linspace(-1, 1, d // 32)
+    host["vs"] *= np.stack([size, size[::-1]])[None, :, None, :].astype(np.float32)
+    host["vs"] = O.bf16_round(host["vs"])
+    q = torch.randn(1, 2 * Hq, 1, d, generator=torch.Generator().manual_seed(Hq)).bfloat16()
+    both(cuda_lib, q, host, [391], d ** -0.5, f"groups {spread} apart", splits=(1, 0, 3))

@@ -139,8 +139,10 @@ __device__ __forceinline__ uint32_t kv4_word(const uint2& w, int i) { return i ?
 __device__ __forceinline__ uint32_t kv4_word(const uint32_t& w, int) { return w; }
 
 // the words of a row's scales times powers of two, exact as long as the product is normal
-__device__ __forceinline__ void kv4_scale_words(uint2& w, uint32_t up) { w.x = mul_bf16x2(w.x, up), w.y = mul_bf16x2(w.y, up); }
-__device__ __forceinline__ void kv4_scale_words(uint32_t& w, uint32_t up) { w = mul_bf16x2(w, up); }
+__device__ __forceinline__ void kv4_scale_words(uint2& w, const uint32_t (&up)[2]) {
+  w.x = mul_bf16x2(w.x, up[0]), w.y = mul_bf16x2(w.y, up[1]);
+}
+__device__ __forceinline__ void kv4_scale_words(uint32_t& w, const uint32_t (&up)[1]) { w = mul_bf16x2(w, up[0]); }
 // 2^n as a float, 0 below the normal numbers; n <= 127
 __device__ __forceinline__ float kv4_exp2i(int n) { return n < -126 ? 0.f : __uint_as_float((uint32_t)(127 + n) << 23); }
 
@@ -162,9 +164,9 @@ __device__ __forceinline__ float kv4_exp2i(int n) { return n < -126 ? 0.f : __ui
 //   O^T = V^T P^T, rows = channels, columns = heads: B is p times the slot's scale
 //     of the group, rounded to fp16 (the one rounding of P, 2^-11), with the
 //     scale taken times a power of two that keeps p s below 2^15.  That power follows
-//     the largest scale met so far as the running max follows the scores, so
-//     a product counts from 2^-32 of the largest scale on; it never touches p or the
-//     sum of p, which know nothing of the values.  The offset goes out 16
+//     the largest scale of the group met so far as the running max follows the scores, so
+//     a product counts from 2^-32 of its group's largest scale on; it never touches p or
+//     the sum of p, which know nothing of the values.  The offset goes out 16
 //     slots at a time through a second product with the constant -8: summed up over
 //     a long row it would swamp the result.  What the cancellation leaves is below
 //     2^-15 of p times the scale (a step of the grid), far inside the format's own
@@ -349,10 +351,12 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
   // per head 2t, 2t + 1: reference max of y (scores before fx), threshold above which
-  // it moves, exponent M that probabilities are taken against.  vref: 2^ev, bf16x2, no
-  // scale so far is larger; vup: 2^(15 - ev)
+  // it moves, exponent M that probabilities are taken against.  vref: 2^ev of each two
+  // groups, bf16x2, no scale so far is larger; vup: 2^(15 - ev)
   float my[2] = {-INFINITY, -INFINITY}, thr[2] = {-INFINITY, -INFINITY}, M[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
-  uint32_t vref = KV4_VREF0, vup = KV4_VUP - KV4_VREF0;
+  uint32_t vref[NG / 2], vup[NG / 2];
+#pragma unroll
+  for (int w = 0; w < NG / 2; ++w) vref[w] = KV4_VREF0, vup[w] = KV4_VUP - KV4_VREF0;
   const uint32_t flip0 = 0x00080008u, flip1 = 0x00800080u;
   const uint32_t pick = hi ? 0x3244u : 0x1044u;  // PAIR: this lane's half of a word of scales, as a float
 
@@ -470,22 +474,35 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     float h0 = fmaxf(y[0][0], y[0][2]), h1 = fmaxf(y[0][1], y[0][3]);
 #pragma unroll
     for (int u = 1; u < C::U; ++u) h0 = fmax3(h0, y[u][0], y[u][2]), h1 = fmax3(h1, y[u][1], y[u][3]);
-    uint32_t vm = vref;
+    uint32_t vm[NG / 2];
+    bool vmoved = false;
 #pragma unroll
-    for (int u = 0; u < C::U; ++u)
+    for (int w = 0; w < NG / 2; ++w) {
+      vm[w] = vref[w];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int u = 0; u < C::U; ++u)
 #pragma unroll
-        for (int w = 0; w < NG / 2; ++w) vm = max_bf16x2(vm, kv4_word(vs[u][h], w));
-    if (__any_sync(0xffffffffu, h0 > thr[0] || h1 > thr[1] || vm != vref)) {
-      uint32_t v = max(vm & 0xFFFFu, vm >> 16);
+        for (int h = 0; h < 2; ++h) vm[w] = max_bf16x2(vm[w], kv4_word(vs[u][h], w));
+      vmoved |= vm[w] != vref[w];
+    }
+    if (__any_sync(0xffffffffu, h0 > thr[0] || h1 > thr[1] || vmoved)) {
+      // what the outputs of each of the lane's groups shrink by for V's sake
+      float fv[NQ];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-      float fv = 1.f;  // what the outputs so far shrink by for V's sake
-      if (v > (vref & 0xFFFFu)) {
-        const uint32_t up = ((v & 0x7F80u) + 0x80u) * 0x10001u;
-        fv = kv4_exp2i(((int)(vref & 0xFFFFu) - (int)(up & 0xFFFFu)) >> 7);
-        vref = up, vup = KV4_VUP - up;
+      for (int w = 0; w < NG / 2; ++w) {
+        uint32_t v = vm[w];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v = max_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, o));
+        const uint32_t lo = (v & 0xFFFFu) > (vref[w] & 0xFFFFu) ? (v & 0x7F80u) + 0x80u : vref[w] & 0xFFFFu;
+        const uint32_t up = (v >> 16) > (vref[w] >> 16) ? ((v >> 16) & 0x7F80u) + 0x80u : vref[w] >> 16;
+        const float f0 = kv4_exp2i(((int)(vref[w] & 0xFFFFu) - (int)lo) >> 7);
+        const float f1 = kv4_exp2i(((int)(vref[w] >> 16) - (int)up) >> 7);
+        if constexpr (PAIR)
+          fv[w] = hi ? f1 : f0;
+        else
+          fv[2 * w] = f0, fv[2 * w + 1] = f1;
+        vref[w] = lo | up << 16;
+        vup[w] = KV4_VUP - vref[w];
       }
       float mx[2] = {h0, h1};
 #pragma unroll
@@ -502,9 +519,11 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
           M[k] = Mn;
           thr[k] = mx[k] + C::TAU / fx[k];
         }
-        f *= fv;
 #pragma unroll
-        for (int n = 0; n < 2 * NG; ++n) acc[n][k] *= f, acc[n][k + 2] *= f;
+        for (int n = 0; n < 2 * NG; ++n) {
+          const float fn = f * fv[n / (PAIR ? 4 : 2)];
+          acc[n][k] *= fn, acc[n][k + 2] *= fn;
+        }
       }
     }
 #pragma unroll
@@ -587,9 +606,13 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   const size_t part = (size_t)(piece + at.item) * p.per_block;  // unique: the next piece or item has the next number
   // A partial output is divided by its own sum: a mean of values, which no number of
   // slots carries out of range.  2^(24 + ev - 15) over the sum, in three factors
-  float inv[2];
-  const int ev = (int)(vref >> 23) - 127, ev0 = ev / 2;
-  const float back0 = kv4_exp2i(ev0), back1 = kv4_exp2i(ev - ev0);
+  float inv[2], back[NQ][2];
+#pragma unroll
+  for (int g = 0; g < NQ; ++g) {
+    const uint32_t v = PAIR ? vref[g] >> (hi ? 16 : 0) : vref[g / 2] >> (g & 1 ? 16 : 0);
+    const int ev = (int)((v & 0xFFFFu) >> 7) - 127;
+    back[g][0] = kv4_exp2i(ev / 2), back[g][1] = kv4_exp2i(ev - ev / 2);
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k) inv[k] = l[k] == 0.f ? 0.f : 0x1p9f / l[k];
   if constexpr (PAIR) {
@@ -603,7 +626,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         float v[4];
 #pragma unroll
         for (int i4 = 0; i4 < 4; ++i4)  // odd nibbles carry 16
-          v[i4] = (hi ? acc[4 * g + i4][k + 2] : acc[4 * g + i4][k]) * ((i4 & 1) ? inv[k] * 0.0625f : inv[k]) * back0 * back1;
+          v[i4] = (hi ? acc[4 * g + i4][k + 2] : acc[4 * g + i4][k]) * ((i4 & 1) ? inv[k] * 0.0625f : inv[k]) * back[g][0] * back[g][1];
         *reinterpret_cast<float4*>(o + 64 * g) = make_float4(v[0], v[1], v[2], v[3]);
       }
       if (r == 0 && !hi) p.ml_part[part + h] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
@@ -615,10 +638,11 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     float* o = p.o_part + (part + 2 * t + k) * D + 4 * r;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {  // odd nibbles carry 16
-      const float even = inv[k], odd = inv[k] * 0.0625f;
-      *reinterpret_cast<float4*>(o + 32 * g) =
-          make_float4(acc[2 * g][k] * even * back0 * back1, acc[2 * g][k + 2] * odd * back0 * back1,
-                      acc[2 * g + 1][k] * even * back0 * back1, acc[2 * g + 1][k + 2] * odd * back0 * back1);
+      const float f[2] = {inv[k], inv[k] * 0.0625f};
+      float v[4];
+#pragma unroll
+      for (int i4 = 0; i4 < 4; ++i4) v[i4] = acc[2 * g + i4 / 2][k + 2 * (i4 & 1)] * f[i4 & 1] * back[g][0] * back[g][1];
+      *reinterpret_cast<float4*>(o + 32 * g) = make_float4(v[0], v[1], v[2], v[3]);
     }
     if (r == 0) p.ml_part[part + 2 * t + k] = make_float2(my[k] == -INFINITY ? -INFINITY : M[k], l[k]);
   }
