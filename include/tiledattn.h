@@ -436,8 +436,8 @@ ATTN_API int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn
  * cache heads, live slots [0, seqlens[b]).  With weights, every live slot's
  * weight grows by the sum of the softmax probabilities of its cache head's
  * query heads.  A sequence without live slots gets O = 0, LSE = -inf.  A live
- * slot that reads as NaN makes its heads' rows NaN; so does a query channel of
- * 2^112 or more.  seqlens must not change while the call runs.
+ * slot that reads as NaN makes its heads' rows NaN.  seqlens must not change
+ * while the call runs.
  *   q, o bf16 [B][Hq][1][d]; lse fp32 [B][Hq]; seqlens int32 [B] DEVICE;
  *   weights fp32 [B][Hkv][capacity], 16-byte aligned, or NULL; num_splits, 1 to 1024: the live
  *   slots of the whole batch are cut into at most num_splits * B * Hkv equal

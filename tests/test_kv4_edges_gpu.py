@@ -1,5 +1,5 @@
-"""GPU parity of the 4-bit cache's decode where values are of very different sizes,
-against an fp64 computation of the definition.
+"""GPU parity of the 4-bit cache's decode where values, scales and queries
+are of very different sizes, against an fp64 computation of the definition.
 
 Tolerances, from the arithmetic (p: probability, s: scale of v's group, n: slots):
 
@@ -126,3 +126,27 @@ def test_groups_of_very_different_size(cuda_lib, Hq, d, spread):
     host["vs"] = O.bf16_round(host["vs"])
     q = torch.randn(1, 2 * Hq, 1, d, generator=torch.Generator().manual_seed(Hq)).bfloat16()
     both(cuda_lib, q, host, [391], d ** -0.5, f"groups {spread} apart", splits=(1, 0, 3))
+
+
+# ------------------------------------------------------------------ queries and scales of any size
+@pytest.mark.parametrize("Hq,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("q_size,k_size,scale", [
+    (112, -112, 0.1), (119, -119, 0.1), (125, -124, 0.1), (-125, 120, 0.1), (-131, 120, 2.0 ** 7),
+    (60, 60, 2.0 ** -123), (-60, -60, 2.0 ** 117), (0, 125, 2.0 ** -127), (100, -110, 100.0),
+])
+def test_queries_and_scale_of_any_size(cuda_lib, Hq, d, q_size, k_size, scale):
+    """Powers of two that cancel in the scores: the same accuracy as without them."""
+    host = case(1, 96, d, 4)
+    host["ks"] = O.bf16_round(np.minimum(host["ks"], 0.5).astype(np.float64) * 2.0 ** k_size)
+    q = torch.randn(1, Hq, 1, d, generator=torch.Generator().manual_seed(7)).clamp(-3, 3).double() * 2.0 ** q_size
+    both(cuda_lib, q.bfloat16(), host, [93], scale, f"q 2^{q_size}, k 2^{k_size}")
+
+
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -133])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -40, 2.0 ** -126])
+def test_queries_of_next_to_nothing(cuda_lib, size, scale):
+    """Every live slot gets the same probability, dead ones of the tile none."""
+    for d, Hq in ((128, 3), (64, 6)):
+        host = case(1, 96, d, 5)
+        q = torch.full((1, Hq, 1, d), size, dtype=torch.float64).bfloat16()
+        both(cuda_lib, q, host, [75], scale, f"q {size}")

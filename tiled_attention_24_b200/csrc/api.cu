@@ -1114,7 +1114,7 @@ int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn_bf16_t* 
   p.blocks = (p.group + 7) / 8;
   p.per_block = std::min(8, p.group);
   p.pieces = (int)kv4_pieces(B, Hq, Hkv, capacity, num_splits);
-  p.sl2 = scale * 1.4426950408889634f;
+  p.sl2 = (float)std::frexp(scale * 1.4426950408889634, &p.sl2_exp);
   p.timeout_ns = g_wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = d == 128 ? launch_decode_kv4<4>(p, o, lse, weights, st) : launch_decode_kv4<2>(p, o, lse, weights, st);

@@ -41,7 +41,8 @@ struct DecKv4Params {
   int blocks;                    // blocks of <= 8 query heads per cache head
   int per_block;                 // heads of a block: min(8, group)
   int pieces;
-  float sl2;
+  float sl2;                     // scale log2(e) = sl2 2^sl2_exp
+  int sl2_exp;
   unsigned long long timeout_ns;
 };
 
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
   uint32_t qb[NQ][PAIR ? 8 : 4];
   float c0[NQ][4];  // accumulator start of heads 2t, 2t + 1, once for each slot of the lane
   float fx[2];
+  int far_exp[2];
   {
     uint4 w[NG];
     uint32_t m = 0;
@@ -299,8 +301,9 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // largest channel in [2^e, 2^(e+1)) (below the normal numbers: e = -126); a
-    // head with an infinity or a NaN is left as it is, its outputs are NaN anyway
-    const int e = m >= 0x7F80u ? 14 : max(1, (int)(m >> 7)) - 127;
+    // head with an infinity or a NaN is left as it is, its outputs are NaN anyway; so is
+    // one of zeros, whose scores are 0 at any size
+    const int e = m == 0u || m >= 0x7F80u ? 14 : max(1, (int)(m >> 7)) - 127;
     const int e0 = (14 - e) / 2;  // 2^(14 - e) in two factors
     const float up0 = __uint_as_float((uint32_t)(127 + e0) << 23), up1 = __uint_as_float((uint32_t)(127 + 14 - e - e0) << 23);
 #pragma unroll
@@ -339,11 +342,16 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
       // or every product would start with four moves
       asm volatile("" : "+f"(c0[g][0]), "+f"(c0[g][1]), "+f"(c0[g][2]), "+f"(c0[g][3]));
     }
-    // x = score * sl2 * 2^(24 + e - 14); infinite (and the outputs NaN) only for
-    // queries beyond 2^112
-    const float f = p.sl2 * __uint_as_float((uint32_t)min(254, 127 + 10 + e) << 23);
+    // x = y sl2 2^(sl2_exp + 24 + e - 14).  Of that power fx holds what keeps it far from
+    // 0 and infinity; the rest, if any (queries or scales of extreme size), goes into
+    // y as soon as it is there
+    const int exponent = p.sl2_exp + 10 + e, near_exp = max(-60, min(60, exponent));
+    const float f = p.sl2 * kv4_exp2i(near_exp);
     fx[0] = __shfl_sync(0xffffffffu, f, 8 * t), fx[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+    far_exp[0] = __shfl_sync(0xffffffffu, exponent - near_exp, 8 * t);
+    far_exp[1] = __shfl_sync(0xffffffffu, exponent - near_exp, 8 * t + 4);
   }
+  const bool any_far = __any_sync(0xffffffffu, (far_exp[0] | far_exp[1]) != 0);
 
   float acc[2 * NG][4];
 #pragma unroll
@@ -442,6 +450,14 @@ __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS
         y[u][1] = g ? fmaf(s[1], f0, y[u][1]) : s[1] * f0;
         y[u][2] = g ? fmaf(s[2], f1, y[u][2]) : s[2] * f1;
         y[u][3] = g ? fmaf(s[3], f1, y[u][3]) : s[3] * f1;
+      }
+    }
+    if (any_far) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float f0 = kv4_exp2i(far_exp[k] / 2), f1 = kv4_exp2i(far_exp[k] - far_exp[k] / 2);
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) y[u][k] = y[u][k] * f0 * f1, y[u][k + 2] = y[u][k + 2] * f0 * f1;
       }
     }
     T vs[C::U][2];
