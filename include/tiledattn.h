@@ -480,7 +480,8 @@ ATTN_API int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const 
 /*
  * attn_kv4_evict -- shrink every (batch, cache head) with more than n_keep live
  * slots to n_keep: kept are the slots whose position is at least
- * next_pos[b] - n_recent, then those of the largest weight; equal weights go
+ * next_pos[b] - n_recent, whatever their weight (the lower slots of them, should
+ * they be more than n_keep), then those of the largest weight; equal weights go
  * to the lower slot, -0 equals +0, a NaN weight ranks with -infinity.  In place
  * and without a copy of the cache: kept slots below n_keep stay where they
  * are, the r-th kept slot at or beyond n_keep moves into the r-th free slot

@@ -128,8 +128,8 @@ def evict(weights, positions, seqlens, next_pos, n_keep, n_recent):
                 kept[b, h, :n] = np.arange(n)
                 continue
             w = [(-np.inf if np.isnan(x) else float(x)) for x in weights[b, h, :n]]
-            w = [np.inf if int(p) >= int(next_pos[b]) - n_recent else x for x, p in zip(w, positions[b, h, :n])]
-            stay = set(sorted(range(n), key=lambda j: (-w[j], j))[:n_keep])
+            older = [int(p) < int(next_pos[b]) - n_recent for p in positions[b, h, :n]]
+            stay = set(sorted(range(n), key=lambda j: (older[j], -w[j] if older[j] else 0.0, j))[:n_keep])
             movers = iter(j for j in range(n_keep, n) if j in stay)
             kept[b, h] = [j if j in stay else next(movers) for j in range(n_keep)]
     return kept

@@ -24,7 +24,7 @@ import pytest
 import torch
 
 from oracle import kv4 as O
-from tests.test_kv4_gpu import ints, make_cache, run_decode, to_bf16
+from tests.test_kv4_gpu import ints, make_cache, run_decode, run_evict, to_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +150,30 @@ def test_queries_of_next_to_nothing(cuda_lib, size, scale):
         host = case(1, 96, d, 5)
         q = torch.full((1, Hq, 1, d), size, dtype=torch.float64).bfloat16()
         both(cuda_lib, q, host, [75], scale, f"q {size}")
+
+
+# ------------------------------------------------------------------ eviction
+def keep_by_rule(weights, positions, n, next_pos, n_keep, n_recent):
+    """Which of n slots stay, from the contract: the newest first, then the largest weights,
+    a NaN with -infinity, the lower slot among equals."""
+    newest = [j for j in range(n) if positions[j] >= next_pos - n_recent]
+    rest = [j for j in range(n) if positions[j] < next_pos - n_recent]
+    rest.sort(key=lambda j: (np.inf if np.isnan(weights[j]) else -weights[j], j))
+    return set((newest + rest)[:n_keep])
+
+
+def test_newest_slots_stay_before_infinite_weights(cuda_lib):
+    """A weight of +infinity pins a slot behind the newest ones, not before them."""
+    B, Hkv, cap, d = 2, 3, 2064, 64
+    g = torch.Generator().manual_seed(9)
+    pool = torch.tensor([float("inf")] * 6 + [1.0, 0.0, -float("inf"), float("nan")])
+    w = pool[torch.randint(0, len(pool), (B, Hkv, cap), generator=g)]
+    pos = torch.stack([torch.randperm(cap, generator=g) for _ in range(B * Hkv)]).reshape(B, Hkv, cap).int()
+    _, dev = make_cache(B, Hkv, cap, d, 6)
+    for lens, n_keep, n_recent in (([2060, 3], 2, 1), ([2060, 1500], 40, 40), ([2064, 2001], 700, 64), ([900, 1024], 800, 300)):
+        kept = run_evict(cuda_lib, dev, w.cuda(), pos.cuda(), ints(lens), ints([cap] * B), n_keep, n_recent)[3].cpu().numpy()
+        assert np.array_equal(kept, O.evict(w.numpy(), pos.numpy(), lens, [cap] * B, n_keep, n_recent))
+        for b, n in enumerate(lens):
+            for h in range(Hkv):
+                want = keep_by_rule(w[b, h].numpy(), pos[b, h].numpy(), n, cap, n_keep, n_recent)
+                assert set(kept[b, h].tolist()) - {-1} == want, (b, h, n_keep)

@@ -237,10 +237,10 @@ struct Kv4EvictParams {
   int Hkv, cap, n_keep, n_recent;
 };
 
-// Rank of a slot as an unsigned key: the newest slots on top, then by weight
-// (-0 equals +0, a NaN ranks with -infinity).
+// Rank of a slot as an unsigned key: the newest slots on top, above +infinity (whose
+// key is 0xFF800000), then by weight (-0 equals +0, a NaN ranks with -infinity).
 __device__ __forceinline__ uint32_t kv4_rank_key(float w, int pos, long long first_recent) {
-  if (pos >= first_recent) w = INFINITY;
+  if (pos >= first_recent) return 0xFFFFFFFFu;
   if (w != w) w = -INFINITY;
   const uint32_t b = __float_as_uint(w + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
