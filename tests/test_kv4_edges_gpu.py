@@ -177,3 +177,17 @@ def test_newest_slots_stay_before_infinite_weights(cuda_lib):
             for h in range(Hkv):
                 want = keep_by_rule(w[b, h].numpy(), pos[b, h].numpy(), n, cap, n_keep, n_recent)
                 assert set(kept[b, h].tolist()) - {-1} == want, (b, h, n_keep)
+
+
+# ------------------------------------------------------------------ key weights
+def test_key_weights_without_query_heads(cuda_lib):
+    """The empty sum: zero, or what was there before."""
+    k = torch.randn(2, 3, 40, 64).bfloat16().cuda()
+    q = torch.empty(2, 0, 7, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 0, 7, device="cuda")
+    w = torch.rand(2, 3, 48, device="cuda")
+    before = w.clone()
+    cuda_lib.attn_key_weights(q, k, lse, w, True, 0.1, accumulate=True)
+    assert torch.equal(w, before)
+    cuda_lib.attn_key_weights(q, k, lse, w, True, 0.1)
+    assert not w[..., :40].any() and torch.equal(w[..., 40:], before[..., 40:])

@@ -1154,16 +1154,17 @@ int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const float* ls
   if (rc != ATTN_OK) return rc;
   if (weights_stride < Nkv) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  if (B == 0 || Hq == 0 || Nkv == 0) return ATTN_OK;
-  if (!k || !weights || (Nq > 0 && (!q || !lse))) return ATTN_ERR_INVALID_ARG;
-  if (!aligned16(k) || !aligned4(weights) || !aligned4(seqlens) || (Nq > 0 && (!aligned16(q) || !aligned4(lse))) ||
+  if (B == 0 || Nkv == 0) return ATTN_OK;
+  const bool queries = Hq > 0 && Nq > 0;
+  if (!k || !weights || (queries && (!q || !lse))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned4(weights) || !aligned4(seqlens) || (queries && (!aligned16(q) || !aligned4(lse))) ||
       !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
   const size_t need = attn_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nkv, d);
   if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 columns((unsigned)((Nkv + 255) / 256), (unsigned)(B * Hkv));
-  if (Nq == 0) {
+  if (!queries) {  // an empty sum
     if (!accumulate) ta::key_weights_none_kernel<<<columns, 256, 0, st>>>(weights, weights_stride, Nkv);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
