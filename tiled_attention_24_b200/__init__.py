@@ -6,6 +6,7 @@ conveniences that allocate outputs with torch and call the same entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -219,8 +220,9 @@ class KV4Cache:
     attention weights and the positions per slot that an eviction goes by.
 
     ``capacity`` is rounded up to a multiple of 16.  The host keeps an upper bound of
-    the lengths, so that an append that may not fit is refused without a
-    synchronisation (on the device, tokens beyond the capacity would be dropped)."""
+    the lengths, so that an append that fits needs no synchronisation; where the bound
+    has no room left, the lengths are read (one synchronisation), and an append that
+    does not fit is refused (on the device, tokens beyond the capacity would be dropped)."""
 
     def __init__(self, B: int, Hkv: int, capacity: int, d: int, device="cuda", track: bool = True):
         if B < 1 or Hkv < 1 or capacity < 1 or d not in (64, 128):
@@ -239,15 +241,33 @@ class KV4Cache:
         """Append n tokens (k, v bf16 [B,Hkv,n,d]) to every sequence, or the first
         ``counts[b]`` (int32 [B], 0 to n) of them."""
         n = k.shape[2]
-        if self.length_bound + n > self.capacity:
-            raise ValueError(f"{n} more tokens may not fit: up to {self.length_bound} of {self.capacity} slots are in use")
+        bound = self._bound_after(n, counts, stream)
         attn_kv4_append(k, v, self.kc, self.ks, self.vc, self.vs, self.seqlens, counts, self.weights, self.positions,
                         self.next_pos if self.positions is not None else None, stream)
         with _stream_context(stream, k.device):
             by = n if counts is None else counts.clamp(0, n)
             self.seqlens.add_(by)
             self.next_pos.add_(by)
-        self.length_bound += n
+        self.length_bound = bound
+
+    def _bound_after(self, n, counts, stream):
+        """Upper bound of the lengths after an append of n tokens; ValueError where they do not fit."""
+        if self.length_bound + n <= self.capacity:
+            return self.length_bound + n
+        with _stream_context(stream, self.seqlens.device):
+            most = int((self.seqlens + (n if counts is None else counts.clamp(0, n))).max())
+        if most > self.capacity:
+            raise ValueError(f"{n} more tokens may not fit: a sequence would need {most} of {self.capacity} slots")
+        return most
+
+    def reset(self, sequences: torch.Tensor | None = None, stream=None):
+        """Empty the given sequences (bool [B] on the cache's device; default: all), for
+        requests that have ended: their next token goes to slot 0, at position 0."""
+        with _stream_context(stream, self.seqlens.device):
+            for t in (self.seqlens, self.next_pos):
+                t.zero_() if sequences is None else t.masked_fill_(sequences, 0)
+        if sequences is None:
+            self.length_bound = 0
 
     def read(self, n: int | None = None, stream=None):
         """(k, v) of the first n slots (default: the length bound) as bf16 [B,Hkv,n,d]."""
@@ -281,6 +301,8 @@ class KV4Cache:
 
 def _stream_context(stream, device):
     """torch's own small operations (allocation, lengths) on the stream of the kernels."""
+    if device.type != "cuda":
+        return contextlib.nullcontext()
     if stream is None:
         return torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
