@@ -54,3 +54,83 @@ def test_room_is_what_the_sequences_leave(cuda_lib):
     big = rows((B, Hkv, cap, d), 51)
     c.append(big.cuda(), big.cuda())
     assert c.length_bound == cap and c.seqlens.tolist() == [cap] * B
+
+
+def captured(call):
+    """`call` in a graph, captured on a side stream as torch wants it, and not run yet."""
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    return graph
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_replayed_appends_keep_to_the_room(cuda_lib, ragged):
+    """A decode step in a graph: its replays fill the cache, never run over its end, say
+    which tokens found no room, and the host never goes by a bound that they outran."""
+    ta = cuda_lib
+    B, Hkv, Hq, cap, d = 3, 2, 4, 32, 64
+    c = ta.KV4Cache(B, Hkv, cap, d)
+    k = rows((B, Hkv, 20, d), 1)
+    c.append(k.cuda(), k.cuda(), ints([20, 7, 0]))
+    k1, v1, q1 = (rows((B, h, 1, d), 2 + h).cuda() for h in (Hkv, Hkv, Hq))
+    counts = ints([1, 1, 0]) if ragged else None
+    held = {}
+
+    def step():
+        c.append(k1, v1, counts)
+        held["o"], _ = ta.decode_kv4(q1, c)
+    graph = captured(step)
+    assert c.seqlens.tolist() == [20, 7, 0]
+    by = [1, 1, 0] if ragged else [1, 1, 1]
+    for i in range(1, 15):
+        graph.replay()
+        want = [min(cap, x + i * y) for x, y in zip((20, 7, 0), by)]
+        assert c.seqlens.tolist() == want
+        assert c.dropped.tolist() == [max(0, 20 + i - cap), 0, 0]
+        assert c.next_pos.tolist() == [x + i * y for x, y in zip((20, 7, 0), by)]
+    assert torch.isfinite(held["o"][:2].float()).all()
+    same_rows(c, 0, 31, k1[0].cpu(), v1[0].cpu())
+    same_rows(c, 1, 20, k1[1].cpu(), v1[1].cpu())
+    assert c.positions[0, 0].tolist() == list(range(32))
+    assert c.read()[0].shape[2] == cap
+    before = c.kc.clone()
+    with pytest.raises(ValueError, match="no room"):
+        c.append(k1, v1, ints([0, 1, 1]))
+    c.reset(torch.tensor([True, False, False], device="cuda"))
+    assert c.dropped.tolist() == [0, 0, 0]
+    c.append(k1, v1, ints([1, 1, 0]))
+    assert c.seqlens.tolist() == [1, 22, 14 * by[2]]
+    same_rows(c, 0, 0, k1[0].cpu(), v1[0].cpu())
+    assert torch.equal(c.kc[0, :, 1:], before[0, :, 1:])
+    for _ in range(30):
+        graph.replay()
+    with pytest.raises(ValueError):                          # by the lengths, whatever the bound says
+        c.append(k1, v1, ints([0, 1, 0]))
+
+
+def test_a_graph_that_shrinks_the_cache(cuda_lib):
+    ta = cuda_lib
+    B, Hkv, cap, d = 2, 1, 48, 64
+    c = ta.KV4Cache(B, Hkv, cap, d)
+    k = rows((B, Hkv, 16, d), 5).cuda()
+    graph = captured(lambda: c.evict(8, 2))
+    assert c.length_bound == 0
+    c.append(k, k)
+    c.append(k, k)
+    c.append(k, k)
+    with pytest.raises(ValueError, match="may not fit"):
+        c.append(k, k)
+    graph.replay()
+    assert c.seqlens.tolist() == [8, 8] and c.read()[0].shape[2] == 8
+    c.append(k, k)
+    assert c.seqlens.tolist() == [24, 24] and c.read()[0].shape[2] == 24
+
+    def no_length():
+        with pytest.raises(ValueError, match="n has to be given"):
+            c.read()
+        return c.read(16)
+    captured(no_length)

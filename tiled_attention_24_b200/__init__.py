@@ -222,7 +222,13 @@ class KV4Cache:
     ``capacity`` is rounded up to a multiple of 16.  The host keeps an upper bound of
     the lengths, so that an append that fits needs no synchronisation; where the bound
     has no room left, the lengths are read (one synchronisation), and an append that
-    does not fit is refused (on the device, tokens beyond the capacity would be dropped)."""
+    does not fit is refused.
+
+    An append, ``reset`` or ``evict`` captured into a graph moves the lengths at every
+    replay, unseen by the host: from then on they are read at every append outside a graph.
+    A replayed append whose tokens find no room keeps what fits and counts the others in
+    ``dropped`` (int32 [B]); an append outside a graph is refused from then on, until
+    ``reset`` empties those sequences."""
 
     def __init__(self, B: int, Hkv: int, capacity: int, d: int, device="cuda", track: bool = True):
         if B < 1 or Hkv < 1 or capacity < 1 or d not in (64, 128):
@@ -235,43 +241,68 @@ class KV4Cache:
         self.seqlens, self.next_pos = z((B,), torch.int32), z((B,), torch.int32)
         self.weights = z((B, Hkv, capacity), torch.float32) if track else None
         self.positions = z((B, Hkv, capacity), torch.int32) if track else None
+        self.dropped = z((B,), torch.int32)
         self.length_bound = 0
+        self._in_graph = False  # whether a graph may move the lengths
 
     def append(self, k: torch.Tensor, v: torch.Tensor, counts: torch.Tensor | None = None, stream=None):
         """Append n tokens (k, v bf16 [B,Hkv,n,d]) to every sequence, or the first
         ``counts[b]`` (int32 [B], 0 to n) of them."""
         n = k.shape[2]
-        bound = self._bound_after(n, counts, stream)
+        captured = self._capturing(stream)
+        bound = self.capacity if captured else self._bound_after(n, counts, stream)
         attn_kv4_append(k, v, self.kc, self.ks, self.vc, self.vs, self.seqlens, counts, self.weights, self.positions,
                         self.next_pos if self.positions is not None else None, stream)
         with _stream_context(stream, k.device):
             by = n if counts is None else counts.clamp(0, n)
-            self.seqlens.add_(by)
             self.next_pos.add_(by)
+            if captured:
+                room = self.capacity - self.seqlens
+                self.dropped.add_((by - room).clamp_(min=0))
+                by = torch.minimum(room, torch.full_like(room, n) if counts is None else by)
+            self.seqlens.add_(by)
         self.length_bound = bound
 
     def _bound_after(self, n, counts, stream):
         """Upper bound of the lengths after an append of n tokens; ValueError where they do not fit."""
-        if self.length_bound + n <= self.capacity:
+        if self.length_bound + n <= self.capacity and not self._in_graph:
             return self.length_bound + n
         with _stream_context(stream, self.seqlens.device):
-            most = int((self.seqlens + (n if counts is None else counts.clamp(0, n))).max())
+            after = self.seqlens + (n if counts is None else counts.clamp(0, n))
+            most, dropped = torch.stack((after.max(), self.dropped.max())).tolist()
+        if dropped:
+            raise ValueError("tokens of an append in a replayed graph found no room (see dropped): reset those sequences")
         if most > self.capacity:
             raise ValueError(f"{n} more tokens may not fit: a sequence would need {most} of {self.capacity} slots")
         return most
 
+    def _capturing(self, stream):
+        """Whether calls on the stream go into a graph now; the cache then no longer trusts its bound."""
+        with _stream_context(stream, self.seqlens.device):
+            captured = self.seqlens.is_cuda and torch.cuda.is_current_stream_capturing()
+        self._in_graph |= captured
+        return captured
+
     def reset(self, sequences: torch.Tensor | None = None, stream=None):
         """Empty the given sequences (bool [B] on the cache's device; default: all), for
         requests that have ended: their next token goes to slot 0, at position 0."""
+        captured = self._capturing(stream)
         with _stream_context(stream, self.seqlens.device):
-            for t in (self.seqlens, self.next_pos):
+            for t in (self.seqlens, self.next_pos, self.dropped):
                 t.zero_() if sequences is None else t.masked_fill_(sequences, 0)
-        if sequences is None:
+        if sequences is None and not captured:
             self.length_bound = 0
 
     def read(self, n: int | None = None, stream=None):
-        """(k, v) of the first n slots (default: the length bound) as bf16 [B,Hkv,n,d]."""
-        n = self.length_bound if n is None else n
+        """(k, v) of the first n slots (default: the length bound; once a graph may have
+        moved the lengths, the longest one, read from the device) as bf16 [B,Hkv,n,d]."""
+        if n is None:
+            n = self.length_bound
+            if self._capturing(stream):
+                raise ValueError("in a graph n has to be given: the lengths are not known to the host")
+            if self._in_graph:
+                with _stream_context(stream, self.seqlens.device):
+                    n = int(self.seqlens.max())
         out = []
         with _stream_context(stream, self.kc.device):
             for c, s in ((self.kc, self.ks), (self.vc, self.vs)):
@@ -288,6 +319,7 @@ class KV4Cache:
             raise ValueError("this cache does not track weights: nothing to evict by")
         if not 1 <= n_keep <= self.capacity:
             raise ValueError(f"n_keep must be from 1 to {self.capacity}, got {n_keep}")
+        captured = self._capturing(stream)
         with _stream_context(stream, self.kc.device):
             kept = torch.empty((self.B, self.Hkv, n_keep), dtype=torch.int32, device=self.kc.device)
             ws = torch.empty(attn_kv4_evict_workspace_bytes(self.B, self.Hkv, self.capacity, n_keep),
@@ -295,7 +327,8 @@ class KV4Cache:
             attn_kv4_evict(self.kc, self.ks, self.vc, self.vs, self.weights, self.positions, self.seqlens,
                            self.next_pos, self.weights, self.positions, kept, n_recent, ws, stream)
             self.seqlens.clamp_(max=n_keep)
-        self.length_bound = min(self.length_bound, n_keep)
+        if not captured:
+            self.length_bound = min(self.length_bound, n_keep)
         return kept
 
 
