@@ -467,8 +467,11 @@ ATTN_API int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn
  *   (batch, key/value head) (a cache's weights: weights_stride = capacity);
  *   accumulate != 0 adds to what is there, 0 overwrites it.
  *   seqlens int32 [B] DEVICE or NULL: a padded batch; only tokens at positions
- *   below seqlens[b] count (query i has position i + Nkv - Nq), keys beyond get
- *   weight 0.  workspace: attn_key_weights_workspace_bytes(...) bytes (may be
+ *   below seqlens[b] count (query i has position i + Nkv - Nq in every sequence, so
+ *   one that ends before Nkv - Nq has no query in a window), keys beyond get
+ *   weight 0.  lse has to be over the keys that count: with causal the forward's
+ *   is; without, the forward's counts the padding's keys too, so hand an lse that
+ *   leaves them out (attn_fwd_varlen's, sequence by sequence).  workspace: attn_key_weights_workspace_bytes(...) bytes (may be
  *   0), 16-byte aligned.
  */
 ATTN_API size_t attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nkv, int d);

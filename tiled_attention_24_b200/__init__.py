@@ -369,7 +369,9 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, causal: boo
                 out: torch.Tensor | None = None, seqlens: torch.Tensor | None = None, accumulate: bool = False,
                 stream=None):
     """Attention weight each key of a prompt received, fp32 [B,Hkv,Nkv] (or the first Nkv
-    entries of the rows of ``out``, for instance a cache's weights)."""
+    entries of the rows of ``out``, for instance a cache's weights).  ``seqlens`` (int32
+    [B]): a padded batch; without ``causal``, lse then has to leave the padding's keys out,
+    which ``forward`` does not."""
     B, Hq, Nq, d = q.shape
     Hkv, Nkv = k.shape[1], k.shape[2]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
