@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import kv4 as O
-from tests.test_kv4_gpu import bits, ints, to_bf16
+from tests.test_kv4_gpu import bits, check_weights, ints, to_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,67 @@ def test_a_graph_that_shrinks_the_cache(cuda_lib):
             c.read()
         return c.read(16)
     captured(no_length)
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_go_to_the_stream_they_are_given(cuda_lib, raw):
+    """Inputs that arrive late on a side stream: a call that went to the current one would
+    work on zeros, or on a cache that is not written yet."""
+    ta = cuda_lib
+    B, Hq, Hkv, N, d, cap, n_keep = 2, 4, 2, 200, 64, 208, 96
+    data = [rows((B, h, n, d), 20 + i).cuda() for i, (h, n) in enumerate(((Hq, N), (Hkv, N), (Hkv, N), (Hq, 1), (Hkv, 8)))]
+    counts, mask = ints([3, 8]), torch.tensor([True, False], device="cuda")
+
+    def all_calls(c, q, k, v, q1, more, **on):
+        c.append(k, v, **on)
+        _, lse = ta.forward(q, k, v, True, **on)
+        ta.key_weights(q, k, lse, True, out=c.weights, accumulate=True, **on)
+        out = [ta.key_weights(q, k, lse, True, **on), *ta.decode_kv4(q1, c, **on), *c.read(N, **on), c.evict(n_keep, 8, **on)]
+        c.append(more, more, counts, **on)
+        c.reset(mask, **on)
+        return [lse, *out, *ta.decode_kv4(q1, c, **on), c.kc, c.vc, c.ks, c.vs, c.weights, c.positions, c.seqlens, c.next_pos]
+
+    want = all_calls(ta.KV4Cache(B, Hkv, cap, d), *data)
+    late, cache = [torch.zeros_like(x) for x in data], ta.KV4Cache(B, Hkv, cap, d)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                       # about 50 ms
+        for x, y in zip(late, data):
+            x.copy_(y)
+    got = all_calls(cache, *late, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert ta.attn_check_status() == 0
+    for i, (x, y) in enumerate(zip(got, want)):
+        x, y = (t.view(torch.int16) if t.dtype == torch.bfloat16 else t for t in (x, y))
+        assert torch.equal(x, y), i
+
+
+# ------------------------------------------------------------------ the prompt's weights in the cache
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 8, 2), (64, 6, 3)])
+def test_a_prompts_weights_carry_on(cuda_lib, d, Hq, Hkv):
+    """The cache's weights after the prompt and after further steps, against the definition
+    over the same history."""
+    ta = cuda_lib
+    B, N, steps = 2, 300, 4
+    q, k, v = rows((B, Hq, N, d), 41), rows((B, Hkv, N, d), 42), rows((B, Hkv, N, d), 43)
+    c = ta.KV4Cache(B, Hkv, N + steps, d)
+    c.append(k.cuda(), v.cuda())
+    _, lse = ta.forward(q.cuda(), k.cuda(), v.cuda(), True)
+    ta.key_weights(q.cuda(), k.cuda(), lse, True, out=c.weights, accumulate=True)
+    ref, sm = O.key_weights(q, k, lse, True, d ** -0.5)
+    check_weights(c.weights[..., :N], ref, sm, d, N * (Hq // Hkv), "the prompt")
+    total = np.zeros((B, Hkv, c.capacity))
+    total[..., :N] = ref
+    for i in range(steps):
+        k1, v1, q1 = rows((B, Hkv, 1, d), 50 + i), rows((B, Hkv, 1, d), 60 + i), rows((B, Hq, 1, d), 70 + i)
+        c.append(k1.cuda(), v1.cuda())
+        ta.decode_kv4(q1.cuda(), c)
+        host = [t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy() for t in (c.kc, c.ks, c.vc, c.vs)]
+        total += O.decode(q1, *host, [N + i + 1] * B, d ** -0.5)[2]
+    got = c.weights.double().cpu().numpy()
+    # the prompt's bound, the steps' (a factor within 2^-17 where scores stay below 2^4),
+    # and an addition a head and step
+    tol = total * (2 * (d + 16) * 2.0 ** -23 * sm + 2.0 ** -17 + (N * (Hq // Hkv) + steps * Hq) * 2.0 ** -24) + 1e-35
+    assert (np.abs(got - total) <= tol).all() and not got[..., N + steps:].any()

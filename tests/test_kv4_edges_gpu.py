@@ -191,3 +191,36 @@ def test_key_weights_without_query_heads(cuda_lib):
     assert torch.equal(w, before)
     cuda_lib.attn_key_weights(q, k, lse, w, True, 0.1)
     assert not w[..., :40].any() and torch.equal(w[..., 40:], before[..., 40:])
+
+
+# ------------------------------------------------------------------ the rounding of probabilities
+@pytest.mark.parametrize("Hq,d", [(4, 64), (4, 128), (8, 64), (8, 128), (5, 128)])
+def test_probabilities_keep_eleven_bits(cuda_lib, Hq, d):
+    """Two slots with opposite values and about the same probability: the outputs are small
+    beside what they are made of, so that the bound is that of p's own rounding (2^-11, and
+    2^-15 of the codes' offset) and not that of the result's.  The same with p rounded to 8
+    bits is outside of it."""
+    B = 48
+    host, _ = make_cache(B, 1, 16, d, 8)
+    host = {n: v.astype(np.float32) if v.dtype != np.uint8 else v for n, v in host.items()}
+    host["vs"][:, :, 1] = host["vs"][:, :, 0]
+    byte = host["vc"][:, :, 0].astype(np.int64)               # 16 - nibble, both: the negative codes
+    host["vc"][:, :, 1] = (((16 - (byte & 15)) & 15) | ((16 - (byte >> 4)) & 15) << 4).astype(np.uint8)
+    q = torch.randn(B, Hq, 1, d, generator=torch.Generator().manual_seed(d + Hq)).mul(0.5).bfloat16()
+    lens = [2] * B
+    ref = reference(q, host, lens, 0.02)
+    for s in (1, 0):
+        check(run_decode(cuda_lib, q.cuda(), upload(host), ints(lens), 0.02, s), ref, lens, "two slots")
+    o, _, _, pv, grid, ex = ref                              # the oracle's p in 8 bits: seen?
+    far = 0.0
+    for b in range(B):
+        v = O.values(host["vc"][b, 0, :2], host["vs"][b, 0, :2])
+        k = O.values(host["kc"][b, 0, :2], host["ks"][b, 0, :2])
+        x = q[b, :, 0].double().numpy() @ k.T * 0.02
+        p = np.exp(x - x.max(axis=1, keepdims=True))
+        ps = p[:, :, None] * np.repeat(host["vs"][b, 0, :2].astype(np.float64), 32, axis=-1)
+        bf = O.bf16_round(ps.astype(np.float32)) / ps * p[:, :, None]
+        err = np.abs((bf * v).sum(axis=1) / p.sum(axis=1)[:, None] - o[b])
+        tol = (2.0 ** -11 + 2 * ex[b][:, None] + 2.0 ** -20) * pv[b] + grid[b] + 2.0 ** -8 * np.abs(o[b])
+        far = max(far, float(np.nan_to_num(err / np.maximum(tol, 1e-30)).max()))
+    assert far > 1.0
