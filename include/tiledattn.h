@@ -436,8 +436,14 @@ ATTN_API int attn_kv4_read(const uint8_t* codes, const attn_bf16_t* scales, attn
  * cache heads, live slots [0, seqlens[b]).  With weights, every live slot's
  * weight grows by the sum of the softmax probabilities of its cache head's
  * query heads.  A sequence without live slots gets O = 0, LSE = -inf.  A live
- * slot that reads as NaN makes its heads' rows NaN.  seqlens must not change
- * while the call runs.
+ * slot whose K reads as NaN (in any group) makes its heads' O, LSE and weights
+ * NaN, one whose V does the group's channels of their O.  seqlens must not change
+ * while the call runs.  Scores, their maximum, the sums of probabilities, LSE
+ * and weights are fp32 throughout.  For O, a probability times the scale of the
+ * value's group is rounded to fp16 (2^-11 of itself; nothing remains below 2^-32
+ * of the largest scale that the group has had up to there), and the codes enter
+ * as code + 8, whose removal leaves up to 2^-15 of the sum of p times scale per
+ * channel; sums are fp32, the result is rounded to bf16.
  *   q, o bf16 [B][Hq][1][d]; lse fp32 [B][Hq]; seqlens int32 [B] DEVICE;
  *   weights fp32 [B][Hkv][capacity], 16-byte aligned, or NULL; num_splits, 1 to 1024: the live
  *   slots of the whole batch are cut into at most num_splits * B * Hkv equal
@@ -465,7 +471,8 @@ ATTN_API int attn_decode_kv4(const attn_bf16_t* q, const uint8_t* kc, const attn
  *   q bf16 [B][Hq][Nq][d], k bf16 [B][Hkv][Nkv][d], lse fp32 [B][Hq][Nq];
  *   weights: rows of Nkv floats, weights_stride >= Nkv floats apart, one per
  *   (batch, key/value head) (a cache's weights: weights_stride = capacity);
- *   accumulate != 0 adds to what is there, 0 overwrites it.
+ *   accumulate != 0 adds to what is there, 0 overwrites it.  fp32 throughout,
+ *   exponentials within 2^-21 of themselves (the instruction's or a polynomial's).
  *   seqlens int32 [B] DEVICE or NULL: a padded batch; only tokens at positions
  *   below seqlens[b] count (query i has position i + Nkv - Nq in every sequence, so
  *   one that ends before Nkv - Nq has no query in a window), keys beyond get
@@ -494,7 +501,8 @@ ATTN_API int attn_key_weights(const attn_bf16_t* q, const attn_bf16_t* k, const 
  *   entries of the first min(seqlens[b], n_keep) slots are written; they may be
  *   the arrays weights, positions themselves.  Slots >= n_keep are left as
  *   they were.  The caller then sets seqlens[b] to min(seqlens[b], n_keep).
- *   1 <= n_keep <= capacity, 0 <= n_recent <= n_keep; workspace:
+ *   capacity at most 12000000; 1 <= n_keep <= capacity, 0 <= n_recent <= n_keep;
+ *   workspace:
  *   attn_kv4_evict_workspace_bytes(...) bytes, 16-byte aligned.
  */
 ATTN_API size_t attn_kv4_evict_workspace_bytes(int B, int Hkv, int capacity, int n_keep);

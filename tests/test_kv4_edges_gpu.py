@@ -224,3 +224,28 @@ def test_probabilities_keep_eleven_bits(cuda_lib, Hq, d):
         tol = (2.0 ** -11 + 2 * ex[b][:, None] + 2.0 ** -20) * pv[b] + grid[b] + 2.0 ** -8 * np.abs(o[b])
         far = max(far, float(np.nan_to_num(err / np.maximum(tol, 1e-30)).max()))
     assert far > 1.0
+
+
+# ------------------------------------------------------------------ NaN
+@pytest.mark.parametrize("Hq,d", [(4, 64), (4, 128), (8, 64), (8, 128)])
+def test_a_nan_group_reaches_what_reads_it(cuda_lib, Hq, d):
+    """One group of one slot: in V its channels of the head's outputs, in K all that the
+    head's queries give; the other cache head, and everything else, as without it."""
+    n, slot, g = 150, 77, d // 32 - 1
+    host = case(2, 160, d, 9)
+    q = torch.randn(1, 2 * Hq, 1, d, generator=torch.Generator().manual_seed(3)).bfloat16()
+    w0 = torch.zeros(1, 2, 160, device="cuda")
+    for splits in (1, 0):
+        want = run_decode(cuda_lib, q.cuda(), upload(host), ints([n]), 0.1, splits, w0)
+        for side in ("ks", "vs"):
+            bad = {x: y.copy() for x, y in host.items()}
+            bad[side][0, 0, slot, g] = np.nan
+            o, lse, w = run_decode(cuda_lib, q.cuda(), upload(bad), ints([n]), 0.1, splits, w0)
+            first = 0 if side == "ks" else 32 * g
+            assert torch.isnan(o[:, :Hq, :, first:]).all()
+            assert torch.equal(o[:, :Hq, :, :first], want[0][:, :Hq, :, :first]) and torch.equal(o[:, Hq:], want[0][:, Hq:])
+            assert torch.equal(lse[:, Hq:], want[1][:, Hq:]) and torch.equal(w[:, 1], want[2][:, 1])
+            if side == "ks":
+                assert torch.isnan(lse[:, :Hq]).all() and torch.isnan(w[:, 0, :n]).all() and not w[:, 0, n:].any()
+            else:
+                assert torch.equal(lse, want[1]) and torch.equal(w, want[2])

@@ -440,9 +440,11 @@ static int launch_decode_kv4(const ta::DecKv4Params& p, attn_bf16_t* o, float* l
   kernel<<<grid, 32 * ta::KV4_WARPS, ta::DecKv4Cfg<NG>::SMEM, st>>>(p);
   if (cudaPeekAtLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   const long long rows = (long long)p.B * p.Hkv * p.group, heads = (long long)p.B * p.Hkv;
-  // Partials a row, were the sequences alike.  A warp takes 8 in one chain of loads, a
-  // CTA 8 (d = 64: 16) beside one another; over 64 there are few rows, and a CTA
-  // takes 32 channels of one.
+  // Partials a row, were the sequences alike.  A warp takes 4 (d = 64: 8) in one chain of
+  // loads, a CTA 32 (64); over 64 there are few rows, and a CTA takes 32 channels of
+  // one.  A batch of one long sequence among short ones has long rows that a warp merges
+  // all the same (64 sequences, 32 / 8 heads, d = 128, one of 131072 slots: 61 us where the
+  // others are empty, 83 where they have one slot each; alone in its batch 49).
   const long long parts = p.pieces / (heads * p.blocks);
   const int ctas = parts <= 8 ? 0 : parts < 64 ? 1 : NG;
   const long long merge = ctas ? rows * ctas : (rows + W - 1) / W;
@@ -466,7 +468,7 @@ static int launch_kv4_evict(const ta::Kv4EvictParams& p, int heads, cudaStream_t
   const int slice = (per + ta::KV4_EVICT_THREADS - 1) / ta::KV4_EVICT_THREADS * ta::KV4_EVICT_THREADS;
   const bool cached = slice <= ta::KV4_EVICT_CACHED;
   const size_t smem = sizeof(ta::Kv4EvictShared) + (size_t)slice / 8 + (cached ? (size_t)slice * 4 : 0);
-  if (smem > 200 * 1024) return ATTN_ERR_UNSUPPORTED;  // more than 12 million slots
+  if (smem > 200 * 1024) return ATTN_ERR_UNSUPPORTED;  // more than 12029952 slots
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(heads * cl));
   cfg.blockDim = dim3(ta::KV4_EVICT_THREADS);

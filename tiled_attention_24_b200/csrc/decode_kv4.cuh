@@ -19,7 +19,8 @@
 // Bound by the chain of logic operations, products and conversions that makes 4-bit
 // operands (2 warps on a scheduler: fixed latencies, then the ALU pipe at 44 %), not by
 // memory: 64 sequences of 8192 slots, 8 cache heads of 4 query heads, d = 128 (605 MB)
-// take 140 us (4.3 TB/s), 125 with the data in L2, 106 streamed only.
+// take 143 us (4.2 TB/s); 125 with the data in L2 and 106 streamed only where the whole took
+// 140, before each group's scales had a power of two of their own.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -177,8 +178,8 @@ __device__ __forceinline__ float kv4_exp2i(int n) { return n < -126 ? 0.f : __ui
 // the odd group of a pair.  A word of codes (4 channels of each group of the pair)
 // then is an operand as it lies, without bringing a group's halves together, a
 // lane works on the scales of one group of the pair only, and one more addition
-// across lanes joins the scores of the two (64 x 8192 slots, 8 cache heads of 4:
-// 141 us against 143, one row of 131072 slots 53 against 55).
+// across lanes joins the scores of the two (64 x 8192 slots, 8 cache heads of 4, at the
+// time: 141 us against 143, one row of 131072 slots 53 against 55).
 template <int NG, bool PAIR>
 __global__ void __launch_bounds__(32 * DecKv4Cfg<NG>::WARPS, DecKv4Cfg<NG>::CTAS)
     decode_kv4_kernel(const __grid_constant__ DecKv4Params p) {
@@ -720,7 +721,7 @@ __device__ __forceinline__ float2 kv4_row_sum(const DecKv4Params& p, const Kv4Pa
 // What the pieces left becomes the outputs, in one launch.  The first CTAs merge: with
 // f = 2^(M_c - max M), L = sum f l_c, O = sum (f l_c / L) O_c, LSE = ln 2 (max M + log2 L);
 // a row without slots has no partial, a NaN in a live slot stays one.  CTAS = 0: a
-// warp per row, its partials in loads of 8; 1: a CTA per row, a warp (half a warp of
+// warp per row, its partials in loads of 4 (d = 64: of 8); 1: a CTA per row, a warp (half a warp of
 // d = 64) per partial; more: a CTA per 32 channels of a row, 32 partials at a time.
 // The other CTAs, where weights are wanted, take 1024 slots of a cache head each:
 // w_j += sum_h 2^(x_hj - lse_h log2 e), with the rows' log-sum-exps worked out again
