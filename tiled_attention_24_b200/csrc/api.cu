@@ -443,8 +443,8 @@ static int launch_decode_kv4(const ta::DecKv4Params& p, attn_bf16_t* o, float* l
   // Partials a row, were the sequences alike.  A warp takes 4 (d = 64: 8) in one chain of
   // loads, a CTA 32 (64); over 64 there are few rows, and a CTA takes 32 channels of
   // one.  A batch of one long sequence among short ones has long rows that a warp merges
-  // all the same (64 sequences, 32 / 8 heads, d = 128, one of 131072 slots: 61 us where the
-  // others are empty, 83 where they have one slot each; alone in its batch 49).
+  // all the same (32 / 8 heads, d = 128, a sequence of 131072 slots: 40 us alone, 60 beside
+  // 63 empty ones, 83 beside 63 of one slot).
   const long long parts = p.pieces / (heads * p.blocks);
   const int ctas = parts <= 8 ? 0 : parts < 64 ? 1 : NG;
   const long long merge = ctas ? rows * ctas : (rows + W - 1) / W;
